@@ -42,9 +42,6 @@
 // Every wait is bounded (about 2 s of %globaltimer); on expiry the kernel
 // records code 0x6E1 + role in the status word, drains its own TMA copies and
 // MMAs, frees its tensor memory and returns.
-#include <cuda.h>
-#include <cudaTypedefs.h>
-
 #include <cstdlib>
 #include <cstring>
 #include <type_traits>
@@ -52,7 +49,7 @@
 #include "sq_act.cuh"
 #include "sq_common.cuh"
 #include "sq_internal.h"
-#include "sq_wait.cuh"
+#include "sq_tc.cuh"
 
 namespace sq {
 namespace {
@@ -62,7 +59,6 @@ constexpr int BK = 128;  // one 128-byte swizzle row of int8
 constexpr int UMMA_K = 32;
 constexpr int kEpiWarps = 8;  // two per TMEM lane quarter, each on half the tile's columns
 constexpr int kThreads = 64 + 32 * kEpiWarps;
-constexpr uint64_t kTimeoutNs = 2000000000ull;
 // staging: 32 rows x 64 B of data (32 16-bit or 16 32-bit values) + 16 B pad
 // for the plain stores; the TMA-store box uses the first 2 KB of the same
 // slot unpadded (64-byte swizzle), so slots start on 512-byte boundaries.
@@ -202,114 +198,6 @@ __device__ __forceinline__ void tile_coords_b(int tile, const Params& p, int bm,
     tile_coords(tile - b * tpb, p, bm, bn, m0, n0);
 }
 
-// ---------------------------------------------------------------- PTX helpers
-__device__ __forceinline__ uint32_t smem_u32(const void* p) {
-    return static_cast<uint32_t>(__cvta_generic_to_shared(p));
-}
-// Wait for the phase of `parity` to complete, giving up after kTimeoutNs or
-// when another role has aborted (the shared bounded wait of sq_wait.cuh).
-__device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* status,
-                                             int code) {
-    return wait_bounded_ns(bar, parity, abort_flag, status, code, kTimeoutNs);
-}
-
-// The same with the common case inline: one try_wait (which itself suspends
-// the thread for a while if the phase is not complete), and the call into the
-// bounded loop only when that is not enough. The producer and the MMA issuer
-// wait once per k-block; a call per wait sat on their critical path.
-__device__ __forceinline__ bool wait_fast(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* status,
-                                         int code) {
-    if (mbar_try_wait(bar, parity)) return true;
-    return wait_bounded(bar, parity, abort_flag, status, code);
-}
-
-// Short bounded wait used while draining after an abort (ignores the flag).
-__device__ __noinline__ void wait_drain(uint32_t bar, uint32_t parity) {
-    const uint64_t t0 = global_ns();
-    while (!mbar_try_wait(bar, parity))
-        if (global_ns() - t0 > kTimeoutNs / 4) return;
-}
-
-// Tile (x = k, y = row) of problem z of a 3-D [batch, rows, K] int8 tensor
-// into this CTA's shared memory. CG = 2: the completion is counted on the
-// mbarrier `bar` names in the shared::cluster window, which may be the other
-// CTA's of the pair (no multicast: each CTA loads only its own tile).
-template <int CG>
-__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y, int z) {
-    if constexpr (CG == 2) {
-        asm volatile(
-            "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
-            "[%0], [%1, {%3, %4, %5}], [%2];"
-            ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z)
-            : "memory");
-    } else {
-        asm volatile(
-            "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
-            "[%0], [%1, {%3, %4, %5}], [%2];"
-            ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z)
-            : "memory");
-    }
-}
-
-
-// Store a 32 x 32 box of 16-bit outputs (x = column, y = row, z = problem)
-// from this CTA's shared memory; elements outside the tensor are not written.
-__device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, uint32_t src, int x, int y, int z) {
-    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];"
-                 ::"l"(reinterpret_cast<uint64_t>(map)), "r"(src), "r"(x), "r"(y), "r"(z)
-                 : "memory");
-    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-}
-// this thread's bulk stores have finished reading shared memory
-__device__ __forceinline__ void bulk_wait_read_all() {
-    asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-}
-// this thread's bulk stores have completed
-__device__ __forceinline__ void bulk_wait_all() {
-    asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
-}
-
-// ---------------------------------------------------------------- CTA pairs
-__device__ __forceinline__ uint32_t cluster_rank() {
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-// The shared::cluster address of this CTA's shared-memory location `a` in
-// CTA `rank` of the cluster.
-__device__ __forceinline__ uint32_t map_to_rank(uint32_t a, uint32_t rank) {
-    uint32_t r;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(rank));
-    return r;
-}
-// Every thread of both CTAs arrives, then waits (aligned: whole warps).
-__device__ __forceinline__ void cluster_sync_all() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-// Arrive on an mbarrier given by its shared::cluster address (possibly the
-// other CTA's), with the arrive's default semantics. It hands an accumulator
-// buffer back to the pair's MMA issuer: the tensor-memory reads it orders
-// have completed (tcgen05.wait::ld) and are fenced by
-// tcgen05.fence::before_thread_sync, and the issuer's wait is followed by
-// tcgen05.fence::after_thread_sync. A release at cluster scope would first
-// order every earlier memory access of this thread at that scope, a fence per
-// tile that showed up as membar stalls (measured on B200: the int8 QK^T
-// product at 96 x 2048 x 2048 x 128 took 302 us with it, 264 us without).
-__device__ __forceinline__ void mbar_arrive_remote(uint32_t cluster_addr) {
-    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
-}
-
-// UMMA shared-memory descriptor, K-major operand with 128-byte swizzle: rows of
-// 128 bytes, 8-row groups 1024 bytes apart (SBO), version 1, layout 2.
-__device__ __forceinline__ uint64_t sdesc(uint32_t saddr) {
-    uint64_t d = (uint64_t)((saddr & 0x3FFFFu) >> 4);
-    d |= (uint64_t)1 << 16;
-    d |= (uint64_t)(1024 >> 4) << 32;
-    d |= (uint64_t)1 << 46;
-    d |= (uint64_t)2 << 61;
-    return d;
-}
-
 template <int KIND, int CG>
 __device__ __forceinline__ void umma(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
     if constexpr (CG == 2 && KIND == kKindF8) {
@@ -338,65 +226,6 @@ __device__ __forceinline__ void umma(uint32_t d_tmem, uint64_t a, uint64_t b, ui
             ::"r"(d_tmem), "l"(a), "l"(b), "r"(idesc), "r"(acc));
     }
 }
-// Arrive on `bar` once every MMA this thread has issued completes. CG = 2:
-// on the mbarrier at the same shared-memory offset in each CTA of `mask`.
-template <int CG>
-__device__ __forceinline__ void umma_commit(uint32_t bar, uint16_t mask = 3) {
-    if constexpr (CG == 2) {
-        asm volatile(
-            "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
-            ::"r"(bar), "h"(mask)
-            : "memory");
-    } else {
-        asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
-                     : "memory");
-    }
-}
-__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-
-// Issue a 32-column TMEM load without waiting; tmem_wait(r) completes it. The
-// wait names the destination registers so no use of them moves above it.
-__device__ __forceinline__ void tmem_ld32_async(uint32_t taddr, uint32_t* r) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
-          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
-          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-        : "r"(taddr)
-        : "memory");
-}
-__device__ __forceinline__ void tmem_wait(uint32_t* r) {
-    asm volatile("tcgen05.wait::ld.sync.aligned;"
-                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
-                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]),
-                   "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]),
-                   "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]),
-                   "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
-                 :
-                 : "memory");
-}
-
-// A 32-column TMEM load and its wait in one asm statement: the destination
-// registers are defined only after the wait, so the compiler cannot spill or
-// reuse them while the load is in flight.
-__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t* r) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n\t"
-        "tcgen05.wait::ld.sync.aligned;"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
-          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
-          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-        : "r"(taddr)
-        : "memory");
-}
-
 __device__ __forceinline__ float load16(const void* base, int64_t idx, int bf16) {
     const uint16_t u = static_cast<const uint16_t*>(base)[idx];
     if (bf16) return __uint_as_float((uint32_t)u << 16);
@@ -1027,19 +856,6 @@ gemm_w8a8_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_consta
 }
 
 // ---------------------------------------------------------------- host side
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-    if (!fn) {
-        void* ptr = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) ==
-                cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
-    }
-    return fn;
-}
-
 // 3-D int8 tensor [batch, rows, K] (rows of each problem contiguous, problems
 // rows * K bytes apart), box BK x box_rows x 1, 128-byte swizzle.
 bool make_map(CUtensorMap* m, const void* base, int64_t rows, int64_t K, int box_rows, int64_t batch) {
@@ -1052,22 +868,6 @@ bool make_map(CUtensorMap* m, const void* base, int64_t rows, int64_t K, int box
     CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, estr,
                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    return r == CUDA_SUCCESS;
-}
-
-// 3-D 16-bit output [batch, M, ldy] (problems y_bstride elements apart), box
-// 32 columns x 32 rows x 1, 64-byte swizzle (the staging layout of a chunk).
-bool make_map_y(CUtensorMap* m, void* Y, int64_t M, int64_t N, int64_t ldy, int64_t batch, int64_t y_bstride,
-                bool bf16) {
-    auto fn = encode_fn();
-    if (!fn) return false;
-    cuuint64_t dims[3] = {(cuuint64_t)N, (cuuint64_t)M, (cuuint64_t)batch};
-    cuuint64_t strides[2] = {(cuuint64_t)(ldy * 2), (cuuint64_t)(y_bstride * 2)};
-    cuuint32_t box[3] = {32, 32, 1};
-    cuuint32_t estr[3] = {1, 1, 1};
-    CUresult r = fn(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, Y, dims, strides,
-                    box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B,
-                    CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS;
 }
 
