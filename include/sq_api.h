@@ -74,8 +74,13 @@ typedef enum {
     SQ_OP_QUANT_ACT = 1,      /* sq_quantize_act (per-tensor dynamic)       */
     SQ_OP_QUANT_WEIGHT = 2,   /* sq_quantize_weight (per-tensor)            */
     SQ_OP_LLMINT8_DETECT = 3, /* sq_llmint8_detect                          */
-    SQ_OP_LLMINT8 = 4         /* sq_llmint8_matmul                          */
+    SQ_OP_LLMINT8 = 4,        /* sq_llmint8_matmul                          */
+    SQ_OP_GEMM_FP4 = 5,       /* sq_gemm_fp4                                */
+    SQ_OP_KV8_ATTENTION = 6   /* sq_kv8_attention (M = T, N = Hq, K = D)    */
 } sq_op_t;
+
+/* Microscaled 4-bit formats (sq_quantize_*_fp4, sq_gemm_fp4). */
+typedef enum { SQ_NVFP4 = 0, SQ_MXFP4 = 1 } sq_fp4_t;
 
 /* Bytes of workspace an operation needs for the given sizes (0 if none is
  * needed; callers may still pass one). Never fails; unknown op -> 0. */
@@ -89,8 +94,9 @@ SQ_API const char* sq_last_error_string(void);
  * SQ_ERR_TIMEOUT it also zeroes the stream-K counters of the last GEMM that
  * used them on this workspace (their size is recorded in the header), so the
  * workspace is ready for the next call without the caller zeroing it again.
- * Applies to workspaces passed to sq_gemm_w8a8, sq_gemm_fp8, sq_bmm_w8a8,
- * sq_llmint8_matmul and sq_selftest_wait_timeout. */
+ * Applies to workspaces passed to sq_gemm_w8a8, sq_gemm_fp8, sq_gemm_fp4,
+ * sq_bmm_w8a8, sq_llmint8_matmul, sq_kv8_attention and
+ * sq_selftest_wait_timeout. */
 SQ_API sq_status_t sq_workspace_status(void* workspace, sq_stream_t stream);
 
 /* Check of the failure path of the bounded device waits: launches one block
@@ -379,6 +385,104 @@ SQ_API sq_status_t sq_gemm_fp8(const uint8_t* Xq, const uint8_t* Wq, int64_t M, 
                                const float* qs_x, int x_per_token, const float* qs_w, int w_per_channel,
                                const float* bias, sq_dtype_t out_dt, void* Y, int64_t ldy, void* workspace,
                                size_t ws_bytes, sq_stream_t stream);
+
+/* --------------------------------------------------------------------------
+ * Microscaled 4-bit linear layer (no counterpart in the pages: the step below
+ * 8 bits, on the block-scaled units of sm_100a).
+ *   Codes: E2M1 (0, 0.5, 1, 1.5, 2, 3, 4, 6 and negatives), [rows, K/2] uint8,
+ *   contiguous, element 2c in the low and 2c + 1 in the high four bits of byte
+ *   c. Block scales b, one byte per block of a row:
+ *     SQ_NVFP4: blocks of 16, E4M3; and an fp32 scale qs per row beside them
+ *     SQ_MXFP4: blocks of 32, E8M0 (2^(byte - 127)); no scale per row
+ *   An element stands for code * b / qs (MXFP4: code * b).
+ *   Block scales are held in tiles of 128 rows x 4 blocks, sq_fp4_scale_bytes()
+ *   bytes in all: the scale of row r, block c is byte (r % 32) * 16 +
+ *   (r / 32 % 4) * 4 + c % 4 of the 512-byte tile (r / 128) * ceil(blocks / 4) +
+ *   c / 4. Rows and blocks that fill up a tile hold zeros (the quantisers write
+ *   them; sq_gemm_fp4 needs the blocks' ones not to be NaN).
+ * sq_quantize_weight_fp4: v = fp32(W) * s[k]; sq_quantize_act_fp4: v = fp32(X) /
+ *   s[k] (IEEE division); s may be NULL: v = the input. Then per row
+ *     NVFP4: qs = 2^(10 - floor(log2 max|v|)) (max|v| below 2^-100 counts as
+ *       2^-100), or *static_qs with per_token = 0; u = fl(v * qs); per block
+ *       b = E4M3(fl(max|u| / 6)), codes = E2M1(fl(u / b)), zero where b is zero
+ *     MXFP4: b = 2^(floor(log2 max|v|) - 2) (at least 2^-127), codes = E2M1(v / b)
+ *   each conversion to the nearest, ties to even, magnitudes past 448 (6)
+ *   saturated. A block holding a NaN or an infinity gets the scale NaN (0x7F,
+ *   0xFF) and zero codes; max|v| is over the finite values.
+ *   qs_w / qs_x: [rows] fp32 ([1], a copy of *static_qs, with per_token = 0),
+ *   NULL for MXFP4. W, X of dt in {F16, BF16, F32}; s, X, codes and scales 16-
+ *   byte aligned, ldx * element size a multiple of 16; K % 32 == 0.
+ * sq_dequantize_fp4: Y = fl(fl(code * b) * fl(1 / qs)) rounded to out_dt in {F32,
+ *   F16, BF16}; qs: [M] (per_row), [1] or NULL (1). Y, ldy 16-byte aligned.
+ * sq_gemm_fp4: Y = acc * ((1/qs_x) * (1/qs_w)) (+ bias[j]) rounded to out_dt, acc
+ *   the tensor cores' fp32 sum of the products code_x b_x code_w b_w. qs_x: [M]
+ *   (x_per_token), [1] or NULL (1); qs_w: [N] (w_per_channel), [1] or NULL;
+ *   bias: [N] fp32 or NULL. K % 32 == 0; codes and scales 16-byte aligned.
+ *   Workspace: SQ_OP_GEMM_FP4, zeroed once before first use; it holds the status
+ *   word and, for shapes with few tiles, arrival counters (at the same bytes for
+ *   every shape, zero again after every completed call) and the parked partial
+ *   sums of a split k-loop. A smaller one (at least 256 bytes) is accepted and
+ *   splits nothing. Calls sharing one must not run concurrently.
+ * ------------------------------------------------------------------------ */
+SQ_API size_t sq_fp4_scale_bytes(sq_fp4_t fmt, int64_t rows, int64_t K);
+SQ_API sq_status_t sq_quantize_weight_fp4(const void* W, sq_dtype_t dt, int64_t N, int64_t K, const float* s,
+                                          sq_fp4_t fmt, uint8_t* Wq, uint8_t* Ws, float* qs_w, sq_stream_t stream);
+SQ_API sq_status_t sq_quantize_act_fp4(const void* X, sq_dtype_t dt, int64_t M, int64_t K, int64_t ldx,
+                                       const float* s, sq_fp4_t fmt, int per_token, const float* static_qs,
+                                       uint8_t* Xq, uint8_t* Xs, float* qs_x, sq_stream_t stream);
+SQ_API sq_status_t sq_dequantize_fp4(const uint8_t* Xq, const uint8_t* Xs, sq_fp4_t fmt, int64_t M, int64_t K,
+                                     const float* qs, int per_row, sq_dtype_t out_dt, void* Y, int64_t ldy,
+                                     sq_stream_t stream);
+SQ_API sq_status_t sq_gemm_fp4(const uint8_t* Xq, const uint8_t* Xs, const uint8_t* Wq, const uint8_t* Ws,
+                               sq_fp4_t fmt, int64_t M, int64_t N, int64_t K, const float* qs_x, int x_per_token,
+                               const float* qs_w, int w_per_channel, const float* bias, sq_dtype_t out_dt, void* Y,
+                               int64_t ldy, void* workspace, size_t ws_bytes, sq_stream_t stream);
+
+/* --------------------------------------------------------------------------
+ * Attention over a paged int8 cache     lpnh.cn SmoothQuant practice article
+ *     §2.2 (attention's operands in int8; sq_bmm_w8a8 is the two products alone).
+ *   Cache: Kc, Vc [num_blocks, Hkv, block, D] int8 codes, kqs, vqs [num_blocks,
+ *   Hkv] fp32: a scale for each block of tokens and head (value = code / qs).
+ *   Batch: T new tokens of B sequences back to back, sequence b's are tokens
+ *   cu_q[b] .. cu_q[b+1]-1 (cu_q: [B+1] int32, ascending from 0); seq_lens[b]
+ *   (int32) is its length with them; block_table[b, j] (int32, row stride ldb)
+ *   is the cache block of its positions j*block .. j*block+block-1. No block
+ *   that is written belongs to two sequences.
+ *   D is 64 or 128; block 16, 32, 64 or 128. All of these are device pointers.
+ * sq_kv8_append: writes the new tokens' K and V. For block and head, with `kept`
+ *   tokens of the sequence in the block before the call and a = max|x| over the
+ *   new tokens that enter it:  qs' = 127 / max(a, 1e-8), and where kept > 0
+ *   min(qs, that); new codes clip(rne(x * qs'), -127, 127); where kept > 0 and
+ *   qs' < qs the kept codes become clip(rne(code * fl(qs' / qs)), -127, 127).
+ *   With kept = 0 what the block and its scales held before is not looked at. A
+ *   NaN or an infinity in x makes the scale NaN, and so every row that reads the
+ *   block. Tokens behind cu_q[B], positions past max_blocks * block and block
+ *   numbers outside 0 .. num_blocks-1 are not written.
+ *   Kn, Vn: [T, Hkv, D] of dt in {F16, BF16}, token strides ldk, ldv (elements,
+ *   multiples of 8), so K and V may be slices of one QKV matrix.
+ * sq_kv8_attention: new token i of n of a sequence of length len, query head h
+ *   (K/V head h / (Hq / Hkv)): Y = softmax_j(scale * q . K_j / kqs) . V_j / vqs over
+ *   the keys j < len - n + i + 1 (causal != 0) or j < len. A row that sees no key
+ *   is zero. A block number outside the cache makes the rows that would read it
+ *   NaN. Tokens behind cu_q[B] are left as they were.
+ *   Q, Y: [T, Hq, D] of dt in {F16, BF16}, token strides ldq, ldy (multiples of
+ *   8), 16-byte aligned. Scores, maxima, sums and outputs are fp32; the softmax
+ *   weights are rounded to fp16 (2^-11) for the second product.
+ *   max_q: the largest number of new tokens of a sequence, or an upper bound; it
+ *   chooses between kernels, results do not depend on it being exact.
+ *   Workspace: SQ_OP_KV8_ATTENTION (M = T, N = Hq, K = D; the size does not depend
+ *   on lengths), zeroed once before first use, as for sq_gemm_fp4.
+ * ------------------------------------------------------------------------ */
+SQ_API sq_status_t sq_kv8_append(const void* Kn, const void* Vn, sq_dtype_t dt, int64_t T, int64_t Hkv, int64_t D,
+                                 int64_t ldk, int64_t ldv, const int32_t* cu_q, const int32_t* seq_lens, int64_t B,
+                                 const int32_t* block_table, int64_t max_blocks, int64_t ldb, int8_t* Kc, int8_t* Vc,
+                                 float* kqs, float* vqs, int64_t num_blocks, int64_t block, sq_stream_t stream);
+SQ_API sq_status_t sq_kv8_attention(const void* Q, sq_dtype_t dt, int64_t T, int64_t Hq, int64_t Hkv, int64_t D,
+                                    int64_t ldq, const int8_t* Kc, const int8_t* Vc, const float* kqs,
+                                    const float* vqs, int64_t num_blocks, int64_t block, const int32_t* cu_q,
+                                    const int32_t* seq_lens, int64_t B, const int32_t* block_table,
+                                    int64_t max_blocks, int64_t ldb, float scale, int causal, int64_t max_q, void* Y,
+                                    int64_t ldy, void* workspace, size_t ws_bytes, sq_stream_t stream);
 
 /* --------------------------------------------------------------------------
  * LLM.int8() mixed-precision decomposition     [SQ-p5] §2.2, §2.3,

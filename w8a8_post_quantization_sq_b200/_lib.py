@@ -21,6 +21,8 @@ SQ_F32, SQ_F16, SQ_BF16, SQ_I32, SQ_I8 = 0, 1, 2, 3, 4
 SQ_LAYERNORM, SQ_RMSNORM = 0, 1
 SQ_ACT_SWIGLU, SQ_ACT_RELU, SQ_ACT_GELU = 0, 1, 2
 SQ_OP_GEMM, SQ_OP_QUANT_ACT, SQ_OP_QUANT_WEIGHT, SQ_OP_LLMINT8_DETECT, SQ_OP_LLMINT8 = 0, 1, 2, 3, 4
+SQ_OP_GEMM_FP4, SQ_OP_KV8_ATTENTION = 5, 6
+SQ_NVFP4, SQ_MXFP4 = 0, 1
 
 STATUS = {0: "SQ_OK", 1: "SQ_ERR_INVALID_ARG", 2: "SQ_ERR_UNSUPPORTED_SHAPE", 3: "SQ_ERR_ALIGNMENT",
           4: "SQ_ERR_CUDA", 5: "SQ_ERR_TIMEOUT"}
@@ -75,6 +77,15 @@ SIGNATURES = {
     "sq_llmint8_quant_weight": ([_p, _i, _i64, _i64, _p, _p, _p, _p, _p], _i),
     "sq_llmint8_matmul": ([_p, _i, _i64, _i64, _i64, ctypes.POINTER(LLMInt8Weight), _f, _d, _p, _i64, _p, _p, _p,
                            _sz, _p], _i),
+    "sq_fp4_scale_bytes": ([_i, _i64, _i64], _sz),
+    "sq_quantize_weight_fp4": ([_p, _i, _i64, _i64, _p, _i, _p, _p, _p, _p], _i),
+    "sq_quantize_act_fp4": ([_p, _i, _i64, _i64, _i64, _p, _i, _i, _p, _p, _p, _p, _p], _i),
+    "sq_dequantize_fp4": ([_p, _p, _i, _i64, _i64, _p, _i, _i, _p, _i64, _p], _i),
+    "sq_gemm_fp4": ([_p, _p, _p, _p, _i, _i64, _i64, _i64, _p, _i, _p, _i, _p, _i, _p, _i64, _p, _sz, _p], _i),
+    "sq_kv8_append": ([_p, _p, _i, _i64, _i64, _i64, _i64, _i64, _p, _p, _i64, _p, _i64, _i64, _p, _p, _p, _p, _i64,
+                       _i64, _p], _i),
+    "sq_kv8_attention": ([_p, _i, _i64, _i64, _i64, _i64, _i64, _p, _p, _p, _p, _i64, _i64, _p, _p, _i64, _p, _i64,
+                          _i64, _f, _i, _i64, _p, _i64, _p, _sz, _p], _i),
 }
 
 _lib = None
@@ -448,3 +459,120 @@ def sq_llmint8_matmul(X, wstate, threshold, min_ratio, Y, idx, n, ws, stream=Non
     _check("sq_llmint8_matmul", lib().sq_llmint8_matmul(
         _ptr(X), _dt(X), M, K, _ld(X), ctypes.byref(wstate["c"]), float(threshold), float(min_ratio), _ptr(Y),
         _ld(Y), _vec(idx, torch.int32, K), _vec(n, torch.int32, 1), _ptr(ws), ws.numel(), _stream(stream)))
+
+
+# ---------------------------------------------------------------- microscaled 4-bit linear layer
+def sq_fp4_scale_bytes(fmt, rows, K):
+    return int(lib().sq_fp4_scale_bytes(fmt, rows, K))
+
+
+def fp4_buffers(rows, K, fmt, device=None):
+    """Codes, block scales and (NVFP4) row scales for a [rows, K] matrix, allocated by torch."""
+    dev = device or "cuda"
+    return (torch.empty((rows, K // 2), dtype=torch.uint8, device=dev),
+            torch.empty(sq_fp4_scale_bytes(fmt, rows, K), dtype=torch.uint8, device=dev),
+            torch.empty(rows, dtype=torch.float32, device=dev) if fmt == SQ_NVFP4 else None)
+
+
+def _fp4(codes, scales, fmt, rows, K, what):
+    _need(fmt in (SQ_NVFP4, SQ_MXFP4), f"unknown format {fmt}")
+    _need(codes.dtype == torch.uint8 and codes.is_contiguous() and tuple(codes.shape) == (rows, K // 2),
+          f"{what}: codes must be contiguous uint8 [{rows}, {K // 2}]")
+    block = 16 if fmt == SQ_NVFP4 else 32
+    need = (rows + 127) // 128 * ((K + 4 * block - 1) // (4 * block)) * 512
+    _need(scales.dtype == torch.uint8 and scales.is_contiguous() and scales.numel() >= need,
+          f"{what}: block scales must be contiguous uint8 of at least {need} bytes")
+
+
+def sq_quantize_weight_fp4(W, s, fmt, Wq, Ws, qs_w, stream=None):
+    N, K = W.shape
+    _need(W.is_contiguous(), "W must be contiguous")
+    _fp4(Wq, Ws, fmt, N, K, "Wq, Ws")
+    _check("sq_quantize_weight_fp4", lib().sq_quantize_weight_fp4(
+        _ptr(W), _dt(W), N, K, _vec(s, torch.float32, K), int(fmt), _ptr(Wq), _ptr(Ws), _vec(qs_w, torch.float32, N),
+        _stream(stream)))
+
+
+def sq_quantize_act_fp4(X, s, fmt, per_token, static_qs, Xq, Xs, qs_x, stream=None):
+    M, K = X.shape
+    _fp4(Xq, Xs, fmt, M, K, "Xq, Xs")
+    _check("sq_quantize_act_fp4", lib().sq_quantize_act_fp4(
+        _ptr(X), _dt(X), M, K, _ld(X), _vec(s, torch.float32, K), int(fmt), int(per_token),
+        _vec(static_qs, torch.float32, 1), _ptr(Xq), _ptr(Xs), _vec(qs_x, torch.float32, M if per_token else 1),
+        _stream(stream)))
+
+
+def sq_dequantize_fp4(Xq, Xs, fmt, qs, Y, stream=None):
+    """qs: [M], [1] or None."""
+    M, K = Y.shape
+    _fp4(Xq, Xs, fmt, M, K, "Xq, Xs")
+    _scales(qs, M, "qs")
+    _check("sq_dequantize_fp4", lib().sq_dequantize_fp4(
+        _ptr(Xq), _ptr(Xs), int(fmt), M, K, _vec(qs, torch.float32), int(qs is not None and qs.numel() > 1), _dt(Y),
+        _ptr(Y), _ld(Y), _stream(stream)))
+
+
+def sq_gemm_fp4(Xq, Xs, Wq, Ws, fmt, qs_x, qs_w, bias, Y, ws, stream=None):
+    """qs_x: [M], [1] or None; qs_w: [N], [1] or None."""
+    M, N = Y.shape
+    K = Xq.shape[1] * 2
+    _fp4(Xq, Xs, fmt, M, K, "Xq, Xs")
+    _fp4(Wq, Ws, fmt, N, K, "Wq, Ws")
+    _scales(qs_x, M, "qs_x")
+    _scales(qs_w, N, "qs_w")
+    _check("sq_gemm_fp4", lib().sq_gemm_fp4(
+        _ptr(Xq), _ptr(Xs), _ptr(Wq), _ptr(Ws), int(fmt), M, N, K, _vec(qs_x, torch.float32),
+        int(qs_x is not None and qs_x.numel() > 1), _vec(qs_w, torch.float32),
+        int(qs_w is not None and qs_w.numel() > 1), _vec(bias, torch.float32, N), _dt(Y), _ptr(Y), _ld(Y), _ptr(ws),
+        ws.numel(), _stream(stream)))
+
+
+# ---------------------------------------------------------------- attention over a paged int8 cache
+def kv8_cache(num_blocks, heads, block, D, device=None):
+    """K codes, V codes, K scales and V scales of an empty cache, allocated by torch."""
+    dev = device or "cuda"
+    codes = [torch.zeros((num_blocks, heads, block, D), dtype=torch.int8, device=dev) for _ in range(2)]
+    return (*codes, *(torch.ones((num_blocks, heads), dtype=torch.float32, device=dev) for _ in range(2)))
+
+
+def _kv8(Kc, Vc, kqs, vqs, cu_q, seq_lens, block_table):
+    nb, heads = Kc.shape[:2]
+    _need(Kc.dtype == torch.int8 and Vc.dtype == torch.int8 and Kc.dim() == 4 and Kc.shape == Vc.shape and
+          Kc.is_contiguous() and Vc.is_contiguous(), "Kc and Vc must be contiguous int8 [num_blocks, Hkv, block, D]")
+    _need(tuple(kqs.shape) == (nb, heads) and tuple(vqs.shape) == (nb, heads), "kqs and vqs must be [num_blocks, Hkv]")
+    B = seq_lens.numel()
+    _need(block_table.dim() == 2 and block_table.dtype == torch.int32 and block_table.shape[0] == B and
+          block_table.stride(1) == 1, f"block_table must be int32 [{B}, max_blocks] with unit inner stride")
+    return (_vec(kqs, torch.float32), _vec(vqs, torch.float32), _vec(cu_q, torch.int32, B + 1),
+            _vec(seq_lens, torch.int32), B)
+
+
+def _heads(t, what):
+    """[T, heads, D] with heads back to back: its token stride."""
+    _need(t.dim() == 3 and t.stride(2) == 1 and t.stride(1) == t.shape[2],
+          f"{what} must be [T, heads, D] with each token's heads back to back")
+    return t.stride(0)
+
+
+def sq_kv8_append(Kn, Vn, cu_q, seq_lens, block_table, Kc, Vc, kqs, vqs, stream=None):
+    """Kn, Vn [T, Hkv, D] (token stride free) into the cache; seq_lens counts the new tokens."""
+    ks, vs, cu, lens, B = _kv8(Kc, Vc, kqs, vqs, cu_q, seq_lens, block_table)
+    T, heads, D = Kn.shape
+    _need(Vn.shape == Kn.shape and Vn.dtype == Kn.dtype, "Kn and Vn must have one shape and dtype")
+    _need(heads == Kc.shape[1] and D == Kc.shape[3], "Kn and the cache must have the same heads and head width")
+    _check("sq_kv8_append", lib().sq_kv8_append(
+        _ptr(Kn), _ptr(Vn), _dt(Kn), T, heads, D, _heads(Kn, "Kn"), _heads(Vn, "Vn"), cu, lens, B, _ptr(block_table),
+        block_table.shape[1], block_table.stride(0), _ptr(Kc), _ptr(Vc), ks, vs, Kc.shape[0], Kc.shape[2],
+        _stream(stream)))
+
+
+def sq_kv8_attention(Q, Kc, Vc, kqs, vqs, cu_q, seq_lens, block_table, scale, causal, max_q, Y, ws, stream=None):
+    """Q, Y [T, Hq, D] (token strides free); max_q: the largest number of new tokens of a sequence."""
+    ks, vs, cu, lens, B = _kv8(Kc, Vc, kqs, vqs, cu_q, seq_lens, block_table)
+    T, hq, D = Q.shape
+    _need(Y.shape == Q.shape and Y.dtype == Q.dtype, "Y must have Q's shape and dtype")
+    _need(D == Kc.shape[3], "Q and the cache must have the same head width")
+    _check("sq_kv8_attention", lib().sq_kv8_attention(
+        _ptr(Q), _dt(Q), T, hq, Kc.shape[1], D, _heads(Q, "Q"), _ptr(Kc), _ptr(Vc), ks, vs, Kc.shape[0], Kc.shape[2],
+        cu, lens, B, _ptr(block_table), block_table.shape[1], block_table.stride(0), float(scale), int(causal),
+        int(max_q), _ptr(Y), _heads(Y, "Y"), _ptr(ws), ws.numel(), _stream(stream)))

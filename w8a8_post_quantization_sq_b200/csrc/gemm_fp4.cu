@@ -1,0 +1,713 @@
+// Product of two microscaled 4-bit matrices on the 5th-generation tensor cores.
+//
+//   acc[i,j] = sum_k (Xq[i,k] bx[i,k/B]) (Wq[j,k] bw[j,k/B])     fp32 sum
+//   Y[i,j]   = acc * ((1/qs_x[i]) (1/qs_w[j])) (+ bias[j]), one rounding
+// with E2M1 codes and block scales b (NVFP4: blocks of 16, E4M3; MXFP4: blocks
+// of 32, E8M0). The tensor core multiplies by the block scales itself
+// (tcgen05.mma kind::mxf4nvf4 / kind::mxf4, K = 64 an instruction).
+//
+// Design: that of the int8 GEMM (a persistent, warp-specialised CTA per SM; one
+// TMA producer thread, one MMA issuer, eight epilogue warps), with
+//   - stages of 256 codes of K (128 bytes a row, 128-byte swizzle), and beside
+//     them the stage's block scales: the scale tiles are in global memory as
+//     tensor memory wants them, so a stage's scales of 128 rows are 2 KB (1 KB)
+//     in one piece;
+//   - the issuer copies each stage's scales to tensor memory (tcgen05.cp, which
+//     runs in issue order with the MMAs around it) and issues the MMAs;
+//   - CTA pairs (256 x 256 tiles): two accumulators of 256 columns and the
+//     scales' 48 (24) columns exceed the 512 of tensor memory, so the second
+//     accumulator starts 48 columns early: the epilogue reads the shared
+//     columns first and hands them back, and the next tile's MMAs start while
+//     the rest is read;
+//   - few tiles (decode batches): the k-loop of each 128 x 128 tile is cut into
+//     equal parts, one CTA each; partial sums are parked in the workspace and
+//     added in part order by the CTA that arrives last.
+// Every wait is bounded (about 2 s), code 0x8E1 + role in the status word.
+#include <cstring>
+#include <type_traits>
+
+#include "sq_common.cuh"
+#include "sq_fp4.cuh"
+#include "sq_internal.h"
+#include "sq_tc.cuh"
+
+namespace sq {
+namespace {
+
+constexpr int BM = 128;
+constexpr int BK = 256;        // codes per stage: 128 bytes, one swizzle row
+constexpr int UMMA_K = 64;     // codes per MMA: 32 bytes
+constexpr int kEpiWarps = 8;   // two per TMEM lane quarter, each on half the tile's columns
+constexpr int kThreads = 64 + 32 * kEpiWarps;
+constexpr int kStgRow = 80;    // staging: 32 rows x 64 B + 16 B pad (the TMA-store box uses the first 2 KB)
+constexpr int kStgWarpBytes = 32 * kStgRow;
+static_assert(kStgWarpBytes % 512 == 0, "staging slots must keep the 64-byte swizzle's 512-byte alignment");
+enum OutKind { kOutBF16 = 0, kOutF16 = 1, kOutF32 = 2 };
+
+template <int FMT, int BN, int CG>
+struct Cfg {
+    static constexpr int STAGES = 5;
+    static constexpr int CHUNKS = FMT == SQ_NVFP4 ? 4 : 2;  // scale tiles (4 blocks) per stage and row group
+    static constexpr int NG = BN / 128;                     // row groups of the weight's scales
+    static constexpr uint32_t A_BYTES = BM * BK / 2;
+    static constexpr uint32_t B_BYTES = (BN / CG) * BK / 2;
+    static constexpr uint32_t SA_BYTES = CHUNKS * kFp4TileBytes;
+    static constexpr uint32_t SB_BYTES = NG * CHUNKS * kFp4TileBytes;
+    static constexpr uint32_t TX = A_BYTES + B_BYTES + SA_BYTES + SB_BYTES;
+    static constexpr uint32_t A_OFF = 0;
+    static constexpr uint32_t B_OFF = A_OFF + STAGES * A_BYTES;
+    static constexpr uint32_t SA_OFF = B_OFF + STAGES * B_BYTES;
+    static constexpr uint32_t SB_OFF = SA_OFF + STAGES * SA_BYTES;
+    static constexpr uint32_t BAR_OFF = SB_OFF + STAGES * SB_BYTES;  // full[S], empty[S], tfull[2], tempty[2], drain
+    static constexpr uint32_t MISC_OFF = BAR_OFF + (2 * STAGES + 5) * 8;
+    static constexpr uint32_t RW_OFF = (MISC_OFF + 16 + 15) / 16 * 16;
+    static constexpr uint32_t RW_BYTES = kEpiWarps * 2 * (BN / 2) * 4;
+    static constexpr uint32_t STG_OFF = (RW_OFF + RW_BYTES + 1023) / 1024 * 1024;
+    static constexpr uint32_t SMEM = STG_OFF + kEpiWarps * kStgWarpBytes;
+    static constexpr uint32_t SMEM_ALLOC = SMEM + 1024;
+    static_assert(SMEM_ALLOC <= 232448, "over the 227 KB of shared memory a block may use");
+    // tensor memory: the scales in the last columns, the accumulators before them
+    static constexpr uint32_t TMEM_COLS = 512;
+    static constexpr uint32_t SB_COLS = CHUNKS * NG * 4;
+    static constexpr uint32_t SFB_COL = TMEM_COLS - SB_COLS;
+    static constexpr uint32_t SFA_COL = SFB_COL - CHUNKS * 4;
+    static constexpr bool OVERLAP = 2 * BN > (int)SFA_COL;
+    static constexpr uint32_t ACC1 = OVERLAP ? SFA_COL - BN : BN;  // first column of the second accumulator
+    static_assert(!OVERLAP || (BN == 256 && BN - ACC1 <= 64), "the shared columns are two 32-column chunks at most");
+    // Instruction descriptor: E2M1 operands (format 1 at bits 7 and 10), K-major,
+    // N >> 3 at bit 17, scale format at bit 23 (0 E4M3, 1 E8M0), M >> 4 at bit
+    // 24; which byte of a scale word to start from: bit 4 (B), bit 29 (A).
+    static constexpr uint32_t idesc(int sf) {
+        return (1u << 7) | (1u << 10) | ((uint32_t)(BN >> 3) << 17) | ((FMT == SQ_MXFP4 ? 1u : 0u) << 23) |
+               ((uint32_t)((BM * CG) >> 4) << 24) | ((uint32_t)sf << 4) | ((uint32_t)sf << 29);
+    }
+};
+
+struct Params {
+    int M, N, K;
+    int num_m, num_n, num_kb;
+    int tiles, splits;
+    int group_m;
+    int vec_store, tma_store;
+    const float* qs_x;
+    const float* qs_w;
+    const float* bias;
+    int x_per_token, w_per_channel;
+    void* Y;
+    int64_t ldy;
+    int* status;
+    int* cnt;      // [tiles][kEpiWarps] parts counted in (zero between launches)
+    float* part;   // [CTA][kEpiWarps][NCH][8][32] float4
+    int cnt_bytes;
+};
+
+__device__ __forceinline__ void tile_coords(int tile, const Params& p, int bm, int bn, int& m0, int& n0) {
+    const int per_group = p.group_m * p.num_n;
+    const int g = tile / per_group;
+    const int r = tile - g * per_group;
+    const int gm0 = g * p.group_m;
+    const int gsize = min(p.group_m, p.num_m - gm0);
+    const int nb = r / gsize;
+    m0 = (gm0 + (r - nb * gsize)) * bm;
+    n0 = nb * bn;
+}
+
+template <int FMT, int CG>
+__device__ __forceinline__ void umma_fp4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa, uint32_t sfb,
+                                         uint32_t acc) {
+    if constexpr (FMT == SQ_NVFP4 && CG == 1)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.block16 [%0], %1, %2, %3, [%5], [%6], p;\n\t}" ::"r"(d),
+            "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(sfa), "r"(sfb));
+    else if constexpr (FMT == SQ_NVFP4)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.block16 [%0], %1, %2, %3, [%5], [%6], p;\n\t}" ::"r"(d),
+            "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(sfa), "r"(sfb));
+    else if constexpr (CG == 1)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.block32 [%0], %1, %2, %3, [%5], [%6], p;\n\t}" ::"r"(d),
+            "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(sfa), "r"(sfb));
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.block32 [%0], %1, %2, %3, [%5], [%6], p;\n\t}" ::"r"(d),
+            "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(sfa), "r"(sfb));
+}
+
+// One scale tile (512 bytes: 32 rows of 16) to four columns of tensor memory,
+// repeated in the four lane quarters; of a pair, each CTA from its own memory.
+template <int CG>
+__device__ __forceinline__ void copy_scales(uint32_t tmem, uint32_t saddr) {
+    // descriptor without swizzle: groups of 8 rows x 16 bytes, 128 bytes apart
+    const uint64_t d = (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(128 >> 4) << 32) | ((uint64_t)1 << 46);
+    if constexpr (CG == 1)
+        asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(d));
+    else
+        asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(d));
+}
+
+template <int OUT>
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+    if constexpr (OUT == kOutBF16) {
+        __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+        return *reinterpret_cast<uint32_t*>(&h);
+    } else {
+        __half2 h = __floats2half2_rn(a, b);
+        return *reinterpret_cast<uint32_t*>(&h);
+    }
+}
+
+// One 32-column chunk of one warp's 32 rows: scale, add the bias, round, stage
+// in shared memory and write out (by TMA store, or whole 64-byte row segments).
+template <int OUT>
+__device__ __forceinline__ void epi_chunk(const Params& p, const uint32_t* r, int cw, int col0, int row0, float rx,
+                                          const float* rw_w, const float* bias_w, uint8_t* stg, int lane,
+                                          const CUtensorMap* tmap_y) {
+    float y[32];
+    const float4* rw4 = reinterpret_cast<const float4*>(rw_w + cw);
+    const uint64_t rx2 = pk2(rx, rx);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const float4 w = rw4[e];
+        const uint64_t d01 = mul2(rx2, pk2(w.x, w.y)), d23 = mul2(rx2, pk2(w.z, w.w));
+        upk2(mul2(pk2(__uint_as_float(r[4 * e]), __uint_as_float(r[4 * e + 1])), d01), y[4 * e], y[4 * e + 1]);
+        upk2(mul2(pk2(__uint_as_float(r[4 * e + 2]), __uint_as_float(r[4 * e + 3])), d23), y[4 * e + 2], y[4 * e + 3]);
+    }
+    if (p.bias) {
+        const float4* b4 = reinterpret_cast<const float4*>(bias_w + cw);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const float4 b = b4[e];
+            y[4 * e + 0] = __fadd_rn(y[4 * e + 0], b.x);
+            y[4 * e + 1] = __fadd_rn(y[4 * e + 1], b.y);
+            y[4 * e + 2] = __fadd_rn(y[4 * e + 2], b.z);
+            y[4 * e + 3] = __fadd_rn(y[4 * e + 3], b.w);
+        }
+    }
+    if constexpr (OUT != kOutF32) {
+        if (p.tma_store) {
+            if (lane == 0) bulk_wait_read_all();
+            __syncwarp();
+            uint8_t* rowp = stg + lane * 64;
+            const int sw = (lane >> 1) & 3;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                *reinterpret_cast<uint4*>(rowp + ((e ^ sw) << 4)) =
+                    make_uint4(pack2<OUT>(y[8 * e], y[8 * e + 1]), pack2<OUT>(y[8 * e + 2], y[8 * e + 3]),
+                               pack2<OUT>(y[8 * e + 4], y[8 * e + 5]), pack2<OUT>(y[8 * e + 6], y[8 * e + 7]));
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) tma_store_3d(tmap_y, smem_u32(stg), col0, row0, 0);
+            return;
+        }
+    }
+    constexpr int HALVES = OUT == kOutF32 ? 2 : 1;
+    constexpr int EB = OUT == kOutF32 ? 4 : 2, EPV = 16 / EB;  // bytes per element, elements per 16 bytes
+#pragma unroll
+    for (int hh = 0; hh < HALVES; ++hh) {
+        uint4* dst = reinterpret_cast<uint4*>(stg + lane * kStgRow);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            if constexpr (OUT == kOutF32)
+                dst[e] = make_uint4(__float_as_uint(y[16 * hh + 4 * e]), __float_as_uint(y[16 * hh + 4 * e + 1]),
+                                    __float_as_uint(y[16 * hh + 4 * e + 2]), __float_as_uint(y[16 * hh + 4 * e + 3]));
+            else
+                dst[e] = make_uint4(pack2<OUT>(y[8 * e], y[8 * e + 1]), pack2<OUT>(y[8 * e + 2], y[8 * e + 3]),
+                                    pack2<OUT>(y[8 * e + 4], y[8 * e + 5]), pack2<OUT>(y[8 * e + 6], y[8 * e + 7]));
+        }
+        __syncwarp();
+        const int part = lane & 3;
+#pragma unroll
+        for (int it = 0; it < 4; ++it) {
+            const int rr = it * 8 + (lane >> 2);
+            const int64_t grow = (int64_t)row0 + rr;
+            const int col = col0 + 16 * hh + part * EPV;
+            const uint4 v = *reinterpret_cast<const uint4*>(stg + rr * kStgRow + part * 16);
+            if (grow < p.M && col < p.N) {
+                uint8_t* out = static_cast<uint8_t*>(p.Y) + (grow * p.ldy + col) * EB;
+                if (p.vec_store && col + EPV <= p.N) {
+                    *reinterpret_cast<uint4*>(out) = v;
+                } else {
+                    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                    for (int e = 0; e < EPV; ++e)
+                        if (col + e < p.N) {
+                            if constexpr (OUT == kOutF32) reinterpret_cast<uint32_t*>(out)[e] = w[e];
+                            else reinterpret_cast<uint16_t*>(out)[e] = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
+                        }
+                }
+            }
+        }
+        __syncwarp();
+    }
+}
+
+template <int FMT, int BN, int CG, int OUT>
+__global__ void __launch_bounds__(kThreads, 1)
+gemm_fp4_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ CUtensorMap tmap_b,
+                const __grid_constant__ CUtensorMap tmap_sa, const __grid_constant__ CUtensorMap tmap_sb,
+                const __grid_constant__ CUtensorMap tmap_y, const Params p) {
+    using C = Cfg<FMT, BN, CG>;
+    constexpr int STAGES = C::STAGES;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t sbase = smem_u32(smem);
+    const uint32_t bar0 = sbase + C::BAR_OFF;
+    auto full_bar = [&](int s) { return bar0 + 8u * s; };
+    auto empty_bar = [&](int s) { return bar0 + 8u * (STAGES + s); };
+    auto tfull_bar = [&](int a) { return bar0 + 8u * (2 * STAGES + a); };
+    auto tempty_bar = [&](int a) { return bar0 + 8u * (2 * STAGES + 2 + a); };
+    const uint32_t drain_bar = bar0 + 8u * (2 * STAGES + 4);
+    uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + C::MISC_OFF);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::MISC_OFF + 4);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = CG == 2 ? cluster_rank() : 0u;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < STAGES; ++s) {
+            mbar_init(full_bar(s), 1);
+            mbar_init(empty_bar(s), 1);
+        }
+        for (int a = 0; a < 2; ++a) {
+            mbar_init(tfull_bar(a), 1);
+            mbar_init(tempty_bar(a), kEpiWarps * CG);
+        }
+        mbar_init(drain_bar, 1);
+        *abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    }
+    if (warp == 1) {
+        if constexpr (CG == 2) {
+            asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;"
+                         ::"r"(smem_u32(tmem_holder)), "r"(C::TMEM_COLS));
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+        } else {
+            asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
+                         ::"r"(smem_u32(tmem_holder)), "r"(C::TMEM_COLS));
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+        }
+    }
+    if (warp == 0 && lane == 0) {
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmap_a)) : "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmap_b)) : "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmap_sa)) : "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmap_sb)) : "memory");
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if constexpr (CG == 2) cluster_sync_all();
+    tc_fence_after();
+    const uint32_t tmem_base = *tmem_holder;
+    pdl_wait();
+    pdl_trigger();
+    if (p.splits > 1 && blockIdx.x == 0 && threadIdx.x == 0) p.status[3] = p.cnt_bytes;
+
+    // this CTA's (or pair's) items: tile w / splits, part w % splits of its k-loop
+    const int first = blockIdx.x / CG, step = gridDim.x / CG, items = p.tiles * p.splits;
+    if (warp == 0) {
+        if (lane == 0) {
+            // ---------------------------------------------------- TMA producer
+            int stage = 0;
+            uint32_t phase = 0, issued = 0, issued_phase = 0;
+            bool ok = true;
+            for (int w = first; ok && w < items; w += step) {
+                const int tile = w / p.splits, part = w - tile * p.splits;
+                const int k0 = (int)((int64_t)part * p.num_kb / p.splits);
+                const int k1 = (int)((int64_t)(part + 1) * p.num_kb / p.splits);
+                int m0, n0;
+                tile_coords(tile, p, BM * CG, BN, m0, n0);
+                const int gn = n0 / 128;
+                m0 += (int)rank * BM;
+                n0 += (int)rank * (BN / CG);
+                for (int kb = k0; kb < k1; ++kb) {
+                    if (!wait_fast(empty_bar(stage), phase ^ 1u, abort_flag, p.status, 0x8E1)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t fb = CG == 2 ? map_to_rank(full_bar(stage), 0) : full_bar(stage);
+                    if (rank == 0) mbar_expect_tx(full_bar(stage), CG * C::TX);
+                    tma_load_3d<CG>(sbase + C::A_OFF + stage * C::A_BYTES, &tmap_a, fb, kb * (BK / 2), m0, 0);
+                    tma_load_3d<CG>(sbase + C::B_OFF + stage * C::B_BYTES, &tmap_b, fb, kb * (BK / 2), n0, 0);
+                    tma_load_3d<CG>(sbase + C::SA_OFF + stage * C::SA_BYTES, &tmap_sa, fb, kb * (int)(C::SA_BYTES / 8),
+                                    m0 / 128, 0);
+                    tma_load_3d<CG>(sbase + C::SB_OFF + stage * C::SB_BYTES, &tmap_sb, fb, kb * (int)(C::SA_BYTES / 8), gn,
+                                    0);
+                    issued |= 1u << stage;
+                    issued_phase = (issued_phase & ~(1u << stage)) | (phase << stage);
+                    if (++stage == STAGES) stage = 0, phase ^= 1u;
+                }
+            }
+            if (!ok && rank == 0)
+                for (int s = 0; s < STAGES; ++s)
+                    if (issued >> s & 1u) wait_drain(full_bar(s), issued_phase >> s & 1u);
+        }
+    } else if (warp == 1) {
+        if (lane == 0 && rank == 0) {
+            // ---------------------------------------------------- MMA issuer
+            int stage = 0, local = 0;
+            uint32_t phase = 0;
+            bool ok = true;
+            for (int w = first; ok && w < items; w += step, ++local) {
+                const int part = w - w / p.splits * p.splits;
+                const int k0 = (int)((int64_t)part * p.num_kb / p.splits);
+                const int k1 = (int)((int64_t)(part + 1) * p.num_kb / p.splits);
+                const int acc = local & 1;
+                // accumulators that share columns: the previous tile's shared
+                // columns (and all of the tile before it) have been read; else
+                // all of the tile before the previous one
+                const int prev = C::OVERLAP ? local - 1 : local - 2;
+                if (prev >= 0 &&
+                    !wait_fast(tempty_bar(prev & 1), (uint32_t)(prev >> 1) & 1u, abort_flag, p.status, 0x8E2)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t d_tmem = tmem_base + (acc ? C::ACC1 : 0u);
+                for (int kb = k0; kb < k1; ++kb) {
+                    if (!wait_fast(full_bar(stage), phase, abort_flag, p.status, 0x8E3)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t a_addr = sbase + C::A_OFF + stage * C::A_BYTES;
+                    const uint32_t b_addr = sbase + C::B_OFF + stage * C::B_BYTES;
+                    const uint32_t sa_addr = sbase + C::SA_OFF + stage * C::SA_BYTES;
+                    const uint32_t sb_addr = sbase + C::SB_OFF + stage * C::SB_BYTES;
+#pragma unroll
+                    for (int c = 0; c < C::CHUNKS; ++c) {
+                        copy_scales<CG>(tmem_base + C::SFA_COL + c * 4, sa_addr + c * kFp4TileBytes);
+#pragma unroll
+                        for (int g = 0; g < C::NG; ++g)
+                            copy_scales<CG>(tmem_base + C::SFB_COL + (c * C::NG + g) * 4,
+                                            sb_addr + (g * C::CHUNKS + c) * kFp4TileBytes);
+                    }
+                    // (codes past K are zero, but so may be all of an MMA's: skip those)
+                    const int steps = min(BK / UMMA_K, (p.K - kb * BK + UMMA_K - 1) / UMMA_K);
+#pragma unroll
+                    for (int k = 0; k < BK / UMMA_K; ++k) {
+                        if (k >= steps) break;
+                        const int c = FMT == SQ_NVFP4 ? k : k >> 1;       // scale tile of this MMA
+                        const int sf = FMT == SQ_NVFP4 ? 0 : (k & 1) * 2;  // first byte of its words
+                        umma_fp4<FMT, CG>(d_tmem, sdesc(a_addr + k * (UMMA_K / 2)), sdesc(b_addr + k * (UMMA_K / 2)),
+                                          C::idesc(sf), tmem_base + C::SFA_COL + c * 4,
+                                          tmem_base + C::SFB_COL + c * C::NG * 4, (kb != k0 || k != 0) ? 1u : 0u);
+                    }
+                    umma_commit<CG>(empty_bar(stage));
+                    if (++stage == STAGES) stage = 0, phase ^= 1u;
+                }
+                if (!ok) break;
+                umma_commit<CG>(tfull_bar(acc));
+            }
+            umma_commit<CG>(drain_bar, 1);
+            wait_drain(drain_bar, 0);
+        }
+    } else {
+        // -------------------------------------------------------- epilogue
+        const int q = warp & 3;
+        const int half = (warp - 2) >> 2;
+        constexpr int HC = BN / 2, NCH = HC / 32;
+        float* rw_w = reinterpret_cast<float*>(smem + C::RW_OFF) + (warp - 2) * 2 * HC;
+        float* bias_w = rw_w + HC;
+        uint8_t* stg = smem + C::STG_OFF + (warp - 2) * kStgWarpBytes;
+        auto release_acc = [&](int a) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                if constexpr (CG == 2) mbar_arrive_remote(map_to_rank(tempty_bar(a), 0));
+                else mbar_arrive(tempty_bar(a));
+            }
+        };
+        int local = 0;
+        for (int w = first; w < items; w += step, ++local) {
+            const int tile = w / p.splits;
+            int m0, n0;
+            tile_coords(tile, p, BM * CG, BN, m0, n0);
+            m0 += (int)rank * BM;
+            const int c_base = n0 + half * HC;
+            const int row0 = m0 + q * 32;
+            const int64_t row = (int64_t)row0 + lane;
+            const bool row_ok = row < p.M;
+            float qv[HC / 32], bv[HC / 32], qxv = 1.0f;
+#pragma unroll
+            for (int i = 0; i < HC / 32; ++i) {
+                const int col = c_base + lane + 32 * i;
+                qv[i] = 1.0f;
+                bv[i] = 0.0f;
+                if (col < p.N) {
+                    if (p.qs_w) qv[i] = p.qs_w[p.w_per_channel ? col : 0];
+                    if (p.bias) bv[i] = p.bias[col];
+                }
+            }
+            if (row_ok && p.qs_x) qxv = p.qs_x[p.x_per_token ? row : 0];
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < HC / 32; ++i) {
+                rw_w[lane + 32 * i] = __frcp_rn(qv[i]);
+                bias_w[lane + 32 * i] = bv[i];
+            }
+            __syncwarp();
+            const int acc = local & 1;
+            // a warp that reads no shared column hands the buffer back at once
+            // (the tile before this one is read in full by now)
+            const bool shares = !C::OVERLAP || half == 1 - acc;
+            if (!shares) release_acc(acc);
+            const bool ok = wait_fast(tfull_bar(acc), (uint32_t)(local >> 1) & 1u, abort_flag, p.status, 0x8E4);
+            if (!__all_sync(0xffffffffu, ok)) break;
+            tc_fence_after();
+            const float rx = __frcp_rn(qxv);
+            const uint32_t t_row =
+                tmem_base + ((uint32_t)(q * 32) << 16) + (acc ? C::ACC1 : 0u) + (uint32_t)(half * HC);
+            uint32_t r[32];
+            if (p.splits > 1) {
+                // park this part's sums; the last of the tile's parts adds
+                // them all up in part order
+                const int wr = warp - 2;
+                constexpr int REGION = NCH * 8 * 32;  // float4 per warp
+                float4* mine = reinterpret_cast<float4*>(p.part) + ((int64_t)w * kEpiWarps + wr) * REGION;
+                for (int c = 0; c < NCH; ++c) {
+                    tmem_ld32(t_row + (uint32_t)(c * 32), r);
+                    if (row_ok)
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            __stcg(mine + (c * 8 + e) * 32 + lane,
+                                   make_float4(__uint_as_float(r[4 * e]), __uint_as_float(r[4 * e + 1]),
+                                               __uint_as_float(r[4 * e + 2]), __uint_as_float(r[4 * e + 3])));
+                }
+                if (shares) release_acc(acc);
+                __threadfence();
+                __syncwarp();
+                int before = 0;
+                int* cnt = p.cnt + tile * kEpiWarps + wr;
+                if (lane == 0) before = atomicAdd(cnt, 1);
+                before = __shfl_sync(0xffffffffu, before, 0);
+                if (before + 1 != p.splits) continue;
+                __threadfence();
+                if (lane == 0) *cnt = 0;  // ready for the next launch
+                for (int c = 0; c < NCH; ++c) {
+                    if (row0 >= p.M || c_base + c * 32 >= p.N) break;
+                    float s[32];
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) s[e] = 0.0f;
+                    if (row_ok)
+                        for (int k = 0; k < p.splits; ++k) {
+                            const float4* src = reinterpret_cast<const float4*>(p.part) +
+                                                (((int64_t)tile * p.splits + k) * kEpiWarps + wr) * REGION;
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) {
+                                const float4 v = __ldcg(src + (c * 8 + e) * 32 + lane);
+                                s[4 * e] += v.x;
+                                s[4 * e + 1] += v.y;
+                                s[4 * e + 2] += v.z;
+                                s[4 * e + 3] += v.w;
+                            }
+                        }
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(s[e]);
+                    epi_chunk<OUT>(p, r, c * 32, c_base + c * 32, row0, rx, rw_w, bias_w, stg, lane, &tmap_y);
+                }
+                continue;
+            }
+            // shared columns first: the upper half's last two chunks of the
+            // first accumulator, the lower half's first two of the second
+            const int turn = C::OVERLAP && acc == 0 && half == 1 ? NCH - 2 : 0;
+#pragma unroll 1
+            for (int i = 0; i < NCH; ++i) {
+                const int c = (i + turn) & (NCH - 1);
+                tmem_ld32(t_row + (uint32_t)(c * 32), r);
+                if (shares && i == (C::OVERLAP ? 1 : NCH - 1)) release_acc(acc);
+                if (row0 < p.M && c_base + c * 32 < p.N)
+                    epi_chunk<OUT>(p, r, c * 32, c_base + c * 32, row0, rx, rw_w, bias_w, stg, lane, &tmap_y);
+            }
+        }
+        if (p.tma_store && lane == 0) bulk_wait_all();
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if constexpr (CG == 2) cluster_sync_all();
+    if (warp == 1) {
+        tc_fence_after();
+        if constexpr (CG == 2)
+            asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(C::TMEM_COLS));
+        else
+            asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(C::TMEM_COLS));
+    }
+}
+
+// ---------------------------------------------------------------- host side
+// Codes [rows, K / 2] bytes, box 128 bytes x box_rows, 128-byte swizzle.
+bool make_map_codes(CUtensorMap* m, const uint8_t* base, int64_t rows, int64_t K, int box_rows) {
+    auto fn = encode_fn();
+    if (!fn) return false;
+    cuuint64_t dims[3] = {(cuuint64_t)(K / 2), (cuuint64_t)rows, 1};
+    cuuint64_t strides[2] = {(cuuint64_t)(K / 2), (cuuint64_t)(rows * K / 2)};
+    cuuint32_t box[3] = {BK / 2, (cuuint32_t)box_rows, 1};
+    cuuint32_t estr[3] = {1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<uint8_t*>(base), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Scale tiles as [row groups, tiles_k * 64] 8-byte words, box chunks * 64 x groups.
+bool make_map_scales(CUtensorMap* m, const uint8_t* base, int64_t groups, int64_t tiles_k, int chunks, int box_groups) {
+    auto fn = encode_fn();
+    if (!fn) return false;
+    cuuint64_t dims[3] = {(cuuint64_t)(tiles_k * 64), (cuuint64_t)groups, 1};
+    cuuint64_t strides[2] = {(cuuint64_t)(tiles_k * kFp4TileBytes), (cuuint64_t)(groups * tiles_k * kFp4TileBytes)};
+    cuuint32_t box[3] = {(cuuint32_t)(chunks * 64), (cuuint32_t)box_groups, 1};
+    cuuint32_t estr[3] = {1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT64, 3, const_cast<uint8_t*>(base), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+struct Plan {
+    int bn = 128, cg = 1, tiles = 0, splits = 1, grid = 0;
+    size_t part_bytes = 0;
+};
+
+// Counters at a fixed place for every shape: one per warp region of a split's
+// tiles, of which there are fewer than SMs.
+constexpr int kMaxSplitTiles = 256;
+constexpr size_t kCntBytes = (size_t)kMaxSplitTiles * kEpiWarps * sizeof(int);
+static_assert(kCntBytes % 256 == 0, "the parked sums start 256-byte aligned");
+
+Plan plan_fp4(int64_t M, int64_t N, int64_t K) {
+    Plan pl;
+    const int sms = num_sms();
+    const int64_t kb = (K + BK - 1) / BK;
+    const int64_t ptiles = ((M + 255) / 256) * ((N + 255) / 256);
+    if (2 * ptiles >= sms) {
+        pl.bn = 256;
+        pl.cg = 2;
+        pl.tiles = (int)ptiles;
+        const int64_t pairs = sms / 2;
+        pl.grid = (int)(2 * (ptiles < pairs ? ptiles : pairs));
+        return pl;
+    }
+    const int64_t tiles = ((M + 127) / 128) * ((N + 127) / 128);
+    pl.tiles = (int)tiles;
+    // equal parts of the k-loop, at least two stages each, while all fit at once
+    int64_t s = sms / tiles;
+    if (s > kb / 2) s = kb / 2;
+    if (s > 16) s = 16;
+    if (s > 1 && tiles <= kMaxSplitTiles) {
+        pl.splits = (int)s;
+        pl.part_bytes = kCntBytes + (size_t)(tiles * s) * BM * 128 * sizeof(float);
+    }
+    pl.grid = (int)(tiles * pl.splits < sms ? tiles * pl.splits : sms);
+    return pl;
+}
+
+struct Call {
+    const uint8_t *Xq, *Xs, *Wq, *Ws;
+    int64_t M, N, K;
+    sq_dtype_t out_dt;
+};
+
+template <int FMT, int BN, int CG, int OUT>
+sq_status_t launch(const char* name, const Call& c, const Plan& pl, Params& p, cudaStream_t stream) {
+    using C = Cfg<FMT, BN, CG>;
+    const int64_t tk = fp4_tiles_k(FMT, c.K);
+    CUtensorMap ta, tb, tsa, tsb, ty;
+    memset(&ty, 0, sizeof(ty));
+    if (!make_map_codes(&ta, c.Xq, c.M, c.K, BM) || !make_map_codes(&tb, c.Wq, c.N, c.K, BN / CG) ||
+        !make_map_scales(&tsa, c.Xs, fp4_tiles_m(c.M), tk, C::CHUNKS, 1) ||
+        !make_map_scales(&tsb, c.Ws, fp4_tiles_m(c.N), tk, C::CHUNKS, C::NG))
+        return set_error(SQ_ERR_CUDA, "%s: cuTensorMapEncodeTiled failed", name);
+    if (OUT != kOutF32 && p.vec_store)
+        p.tma_store = make_map_y(&ty, p.Y, c.M, c.N, p.ldy, 1, c.M * p.ldy, OUT == kOutBF16) ? 1 : 0;
+    p.num_m = (int)((c.M + BM * CG - 1) / (BM * CG));
+    p.num_n = (int)((c.N + BN - 1) / BN);
+    p.num_kb = (int)((c.K + BK - 1) / BK);
+    // rows of X per raster group within about 48 MB of L2
+    const int64_t per = (int64_t)BM * CG * c.K / 2;
+    const int64_t g = (48ll << 20) / per;
+    p.group_m = (int)(g < 1 ? 1 : g > p.num_m ? p.num_m : g);
+    auto fn = gemm_fp4_kernel<FMT, BN, CG, OUT>;
+    if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM_ALLOC) != cudaSuccess)
+        return check_launch(name);
+    if constexpr (CG == 2)
+        launch_pdl_cluster(fn, dim3(pl.grid), dim3(kThreads), C::SMEM_ALLOC, stream, 2, ta, tb, tsa, tsb, ty, p);
+    else
+        launch_pdl(fn, dim3(pl.grid), dim3(kThreads), C::SMEM_ALLOC, stream, ta, tb, tsa, tsb, ty, p);
+    return check_launch(name);
+}
+
+template <int FMT, int OUT>
+sq_status_t launch_plan(const char* name, const Call& c, const Plan& pl, Params& p, cudaStream_t stream) {
+    if (pl.cg == 2) return launch<FMT, 256, 2, OUT>(name, c, pl, p, stream);
+    return launch<FMT, 128, 1, OUT>(name, c, pl, p, stream);
+}
+
+template <int FMT>
+sq_status_t launch_out(const char* name, const Call& c, const Plan& pl, Params& p, cudaStream_t stream) {
+    if (c.out_dt == SQ_BF16) return launch_plan<FMT, kOutBF16>(name, c, pl, p, stream);
+    if (c.out_dt == SQ_F16) return launch_plan<FMT, kOutF16>(name, c, pl, p, stream);
+    return launch_plan<FMT, kOutF32>(name, c, pl, p, stream);
+}
+
+}  // namespace
+
+size_t gemm_fp4_workspace_bytes(int64_t M, int64_t N, int64_t K) {
+    if (M <= 0 || N <= 0 || K <= 0) return kStatusBytes;
+    return kStatusBytes + plan_fp4(M, N, K).part_bytes;
+}
+
+}  // namespace sq
+
+extern "C" sq_status_t sq_gemm_fp4(const uint8_t* Xq, const uint8_t* Xs, const uint8_t* Wq, const uint8_t* Ws,
+                                   sq_fp4_t fmt, int64_t M, int64_t N, int64_t K, const float* qs_x, int x_per_token,
+                                   const float* qs_w, int w_per_channel, const float* bias, sq_dtype_t out_dt, void* Y,
+                                   int64_t ldy, void* workspace, size_t ws_bytes, sq_stream_t stream) {
+    const char* name = "sq_gemm_fp4";
+    SQ_REQUIRE(fmt == SQ_NVFP4 || fmt == SQ_MXFP4, SQ_ERR_INVALID_ARG, "%s: bad format", name);
+    SQ_REQUIRE(out_dt == SQ_F32 || out_dt == SQ_F16 || out_dt == SQ_BF16, SQ_ERR_INVALID_ARG,
+               "%s: out dtype must be F32, F16 or BF16", name);
+    SQ_REQUIRE(M >= 0 && N > 0 && K > 0 && ldy >= N, SQ_ERR_UNSUPPORTED_SHAPE, "%s: need N > 0, K > 0, ldy >= N", name);
+    SQ_REQUIRE(K % 32 == 0, SQ_ERR_UNSUPPORTED_SHAPE, "%s: K must be a multiple of 32", name);
+    SQ_REQUIRE(M < (1ll << 30) && N < (1ll << 30) && K < (1ll << 30) &&
+                   ((M + 127) / 128) * ((N + 127) / 128) < (1ll << 31),
+               SQ_ERR_UNSUPPORTED_SHAPE, "%s: M, N, K must be < 2^30 and the tiles < 2^31", name);
+    if (M == 0) return SQ_OK;
+    SQ_REQUIRE(Xq && Xs && Wq && Ws && Y, SQ_ERR_INVALID_ARG, "%s: null codes, block scales or Y", name);
+    SQ_REQUIRE(sq::aligned16(Xq) && sq::aligned16(Xs) && sq::aligned16(Wq) && sq::aligned16(Ws), SQ_ERR_ALIGNMENT,
+               "%s: codes and block scales must be 16-byte aligned", name);
+    SQ_REQUIRE(workspace && ws_bytes >= sq::kStatusBytes, SQ_ERR_INVALID_ARG, "%s: needs a workspace of %zu bytes", name,
+               sq::kStatusBytes);
+    sq::Plan pl = sq::plan_fp4(M, N, K);
+    if (pl.splits > 1 && ws_bytes < sq::kStatusBytes + pl.part_bytes) {
+        // a workspace without room for the parts runs every k-loop whole
+        pl.splits = 1;
+        pl.grid = pl.tiles < sq::num_sms() ? pl.tiles : sq::num_sms();
+    }
+    const int eb = sq::dtype_bytes(out_dt);
+    sq::Params p;
+    memset(&p, 0, sizeof(p));
+    p.M = (int)M;
+    p.N = (int)N;
+    p.K = (int)K;
+    p.tiles = pl.tiles;
+    p.splits = pl.splits;
+    p.vec_store = sq::aligned16(Y) && (ldy * eb) % 16 == 0;
+    p.qs_x = qs_x;
+    p.qs_w = qs_w;
+    p.bias = bias;
+    p.x_per_token = x_per_token;
+    p.w_per_channel = w_per_channel;
+    p.Y = Y;
+    p.ldy = ldy;
+    p.status = static_cast<int*>(workspace);
+    uint8_t* after = static_cast<uint8_t*>(workspace) + sq::kStatusBytes;
+    p.cnt = reinterpret_cast<int*>(after);
+    p.part = reinterpret_cast<float*>(after + sq::kCntBytes);
+    p.cnt_bytes = (int)sq::kCntBytes;
+    const sq::Call c = {Xq, Xs, Wq, Ws, M, N, K, out_dt};
+    cudaStream_t s = sq::as_cuda(stream);
+    return fmt == SQ_NVFP4 ? sq::launch_out<SQ_NVFP4>(name, c, pl, p, s) : sq::launch_out<SQ_MXFP4>(name, c, pl, p, s);
+}

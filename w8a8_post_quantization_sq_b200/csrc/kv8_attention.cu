@@ -1,0 +1,654 @@
+// Attention over the paged int8 K/V cache (a scale per block of tokens and
+// head), for any number of new tokens per sequence.
+//
+//   s_j = scale q . k_j,  k_j = K_j / kqs(j)      (K_j, V_j: int8 codes)
+//   o   = sum_j w_j v_j,  w = softmax(s),  v_j = V_j / vqs(j)
+// over the keys j < len - n + i + 1 of new token i of n (causal) or j < len.
+//
+// The codes go through the tensor cores as fp16, which holds every int8
+// exactly; the two scales of a block multiply the 16 x 16 score tiles in fp32:
+// the K scale multiplies the scores, and the V scale is folded into the
+// softmax's exponent. With t_j = log2(e) s_j - log2(vqs(j)) and a running
+// maximum m of t (not of s),
+//   P_j = 2^(t_j - m),  O = sum_j P_j V_j,  l = sum_j P_j vqs(j),  o = O / l,
+// so P, the only quantity rounded to fp16, stays below 2^8 whatever the scales,
+// and V is never scaled. P's rounding is at most 2^-11 relative, as that of an
+// fp16 output; m, l, O are fp32. The running maximum is moved only when a
+// score passes it by more than 2^8 (the rescaling of O then costs nothing on
+// most tiles; P <= 256 is far inside fp16).
+// q is scaled by a power of two per row to [1, 2) before it becomes fp16, so a
+// bf16 q keeps its 8 bits (elements 2^14 times smaller than the row's largest
+// lose bits that the fp32 sum could not hold either).
+//
+// Work: rows (new token, query head of the group) of one sequence and K/V head
+// make row tiles of 16; the keys of each row tile are cut into tiles of 64, and
+// the list of all tiles is cut into one contiguous range per block (the lengths
+// are on the device; every block works out its own range). A row tile whose
+// keys fall into several ranges is joined by the block that finishes last,
+// in range order, so results do not depend on timing.
+// In a block, one warp brings 64 keys' K and V by TMA (swizzled, ring of
+// stages), and four warps take 16 keys each; scores and outputs are
+// mma.m16n8k16 (a decode step has 1 to 16 rows per K/V head, an eighth of the
+// smallest tcgen05 tile, and is bound by the cache's bytes).
+#include <cstring>
+
+#include "sq_internal.h"
+#include "sq_kv8.cuh"
+#include "sq_tc.cuh"
+
+namespace sq {
+
+sq_status_t check_kv8(const char* name, int64_t T, int64_t B, int64_t Hkv, int64_t D, int64_t block, int64_t num_blocks,
+                      int64_t max_blocks, int64_t ldb);
+
+namespace {
+
+constexpr int kTile = 64;     // keys per stage
+constexpr int kSub = 16;      // keys per warp of a stage
+constexpr int kCWarps = 4;    // consumer warps
+constexpr int kThreadsA = 32 * (kCWarps + 1);
+constexpr int kStages = 4;
+constexpr int kRows = 16;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kSlack = 8.0f;
+constexpr int kCtasPerSm = 2;
+
+struct AttnArgs {
+    const void* Q;
+    void* Y;
+    int64_t ldq, ldy, T, ldb, num_blocks;
+    const int32_t* cu;
+    const int32_t* lens;
+    const int32_t* table;
+    const float* kqs;
+    const float* vqs;
+    int B, Hkv, G, block, box, max_blocks, causal;
+    float scale;
+    int* status;
+    int* cnt;     // [grid] key tiles counted in per row tile (zero between launches)
+    float* part;  // [grid][2][16][D + 2]: O, then m and l
+};
+
+template <int D>
+struct ACfg {
+    static constexpr uint32_t KV = kTile * D;  // bytes of one stage's K (and of its V)
+    static constexpr uint32_t STAGE = 2 * KV;
+    static constexpr uint32_t SC_OFF = kStages * STAGE;              // float4 [stages][4]: 1/kqs, -log2 vqs, vqs
+    static constexpr uint32_t BAR_OFF = SC_OFF + kStages * 4 * 16;   // full[S], empty[S]
+    static constexpr uint32_t MISC_OFF = BAR_OFF + 2 * kStages * 8;  // abort flag, last flag
+    static constexpr uint32_t ML_OFF = MISC_OFF + 16;                // m, l [warps][16]
+    static constexpr int LDO = D + 4;                                // floats per row of a warp's O
+    static constexpr uint32_t O_OFF = ML_OFF + kCWarps * kRows * 2 * 4;
+    static constexpr uint32_t SMEM = O_OFF + kCWarps * kRows * LDO * 4;
+    static constexpr uint32_t SMEM_ALLOC = SMEM + 1024;
+};
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+    return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+    uint2 v;
+    asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
+    return v;
+}
+// D += A B on 16 x 8 x 16 fp16 with fp32 sums
+__device__ __forceinline__ void mma16816(float* d, const uint32_t* a, uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// Bytes of u (code + 128) as fp16 integers: 0x6400 + u is 1024 + u in fp16, so
+// subtracting 1152 leaves the code, exactly.
+__device__ __forceinline__ uint32_t half2_of(uint32_t u, uint32_t sel) {
+    const uint32_t h = __byte_perm(u, 0x64646464u, sel);
+    uint32_t r;
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(h), "r"(0x64806480u));
+    return r;
+}
+__device__ __forceinline__ uint32_t pack_half2(float a, float b) {
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// One sequence's share of the work.
+struct Seq {
+    int64_t lo;  // first new token
+    int n, len, rt, tiles;
+    __device__ int64_t work(int Hkv) const { return (int64_t)Hkv * rt * tiles; }
+};
+__device__ __forceinline__ Seq seq_of(const AttnArgs& a, int b) {
+    Seq s;
+    const int64_t lo = min(max((int64_t)__ldg(a.cu + b), (int64_t)0), a.T);
+    const int64_t hi = min((int64_t)__ldg(a.cu + b + 1), a.T);
+    s.lo = lo;
+    s.n = (int)max(hi - lo, (int64_t)0);
+    s.len = min(max(__ldg(a.lens + b), 0), a.max_blocks * a.block);
+    s.rt = (int)(((int64_t)s.n * a.G + kRows - 1) / kRows);
+    s.tiles = max((s.len + kTile - 1) / kTile, 1);  // a sequence without keys still has rows to write
+    return s;
+}
+
+// A block's range of the list of key tiles, as pieces: the part of the range
+// inside one row tile. Every warp walks the same sequence.
+struct Walk {
+    int64_t it, end, total, units;
+    int b, item, k0, k1;
+    bool first;
+    Seq s;
+    __device__ __forceinline__ int64_t start_of(int64_t c) const { return c * total / units; }
+    __device__ __forceinline__ int owner_of(int64_t x) const { return (int)(((x + 1) * units + total - 1) / total - 1); }
+
+    __device__ __forceinline__ void init(const AttnArgs& a, int lane) {
+        int64_t sum = 0;
+        for (int i = lane; i < a.B; i += 32) sum += seq_of(a, i).work(a.Hkv);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        total = sum;
+        units = min((int64_t)gridDim.x, total);
+        it = end = 0;
+        b = 0;
+        first = true;
+        if (blockIdx.x >= units) return;
+        it = start_of(blockIdx.x);
+        end = start_of(blockIdx.x + 1);
+        // the sequence that holds `it`
+        int64_t before = 0;
+        for (int base = 0; base < a.B; base += 32) {
+            const int64_t w = base + lane < a.B ? seq_of(a, base + lane).work(a.Hkv) : 0;
+            int64_t inc = w;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int64_t up = __shfl_up_sync(0xffffffffu, inc, o);
+                if (lane >= o) inc += up;
+            }
+            const unsigned past = __ballot_sync(0xffffffffu, before + inc > it);
+            if (past) {
+                const int l = __ffs(past) - 1;
+                b = base + l;
+                before += __shfl_sync(0xffffffffu, inc - w, l);
+                break;
+            }
+            before += __shfl_sync(0xffffffffu, inc, 31);
+        }
+        s = seq_of(a, b);
+        const int64_t r = it - before;
+        item = (int)(r / s.tiles);
+        k0 = (int)(r - (int64_t)item * s.tiles);
+    }
+    // The next piece: tiles [k0, k1) of row tile `item` of sequence b.
+    __device__ __forceinline__ bool next(const AttnArgs& a) {
+        if (it >= end) return false;
+        while (item >= a.Hkv * s.rt) {
+            s = seq_of(a, ++b);
+            item = 0;
+        }
+        k1 = (int)min((int64_t)s.tiles, k0 + (end - it));
+        return true;
+    }
+    __device__ __forceinline__ void done() {
+        it += k1 - k0;
+        first = false;
+        k0 = 0;
+        ++item;
+    }
+    // Keys that the row tile's last row sees, and those that row `row` sees.
+    __device__ __forceinline__ int seen(const AttnArgs& a, int row) const {
+        const int i = min(row / a.G, s.n - 1);
+        return a.causal ? max(min(s.len - s.n + i + 1, s.len), 0) : s.len;
+    }
+};
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreadsA, kCtasPerSm)
+kv8_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
+                     const AttnArgs a) {
+    using C = ACfg<D>;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t sbase = smem_u32(smem);
+    auto full_bar = [&](int s) { return sbase + C::BAR_OFF + 8u * s; };
+    auto empty_bar = [&](int s) { return sbase + C::BAR_OFF + 8u * (kStages + s); };
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::MISC_OFF);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(full_bar(s), 1);
+            mbar_init(empty_bar(s), kCWarps);
+        }
+        *abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    }
+    __syncthreads();
+    pdl_wait();
+    pdl_trigger();
+    Walk w;
+    w.init(a, lane);
+    int stage = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    if (warp == kCWarps) {
+        // ------------------------------------------------------ producer
+        float4* sc = reinterpret_cast<float4*>(smem + C::SC_OFF);
+        const int per_box = a.box / kSub;  // 16-key parts per copy
+        uint32_t issued = 0, issued_phase = 0;
+        for (; ok && w.next(a); w.done()) {
+            const int h = w.item / w.s.rt, rt = w.item - h * w.s.rt;
+            const int vis = w.seen(a, rt * kRows + kRows - 1);
+            const int last = min(w.k1, (vis + kTile - 1) / kTile);
+            const int32_t* row = a.table + (int64_t)w.b * a.ldb;
+            // lane l looks after part l of eight tiles' 32 parts
+            for (int t0 = w.k0; ok && t0 < last; t0 += 8) {
+                const int key = t0 * kTile + lane * kSub;
+                int64_t blk = -1;
+                float kq = __uint_as_float(0x7fffffffu), vq = kq;
+                if (key < vis) {
+                    blk = __ldg(row + key / a.block);
+                    if (blk >= 0 && blk < a.num_blocks) {
+                        kq = __ldg(a.kqs + blk * a.Hkv + h);
+                        vq = __ldg(a.vqs + blk * a.Hkv + h);
+                    } else {
+                        blk = -1;  // no such block: NaN scales, nothing read
+                    }
+                }
+                const float4 mine = make_float4(__frcp_rn(kq), -__log2f(vq), vq, 0.0f);
+                const int y = h * a.block + (key & (a.block - 1));
+                for (int t = t0; t < min(t0 + 8, last); ++t) {
+                    ok = wait_fast(empty_bar(stage), phase ^ 1u, abort_flag, a.status, 0x7E1);
+                    if (!__all_sync(0xffffffffu, ok)) {
+                        ok = false;
+                        break;
+                    }
+                    const int sub = lane - (t - t0) * 4;
+                    const bool mine_now = sub >= 0 && sub < 4;
+                    const bool copy = mine_now && blk >= 0 && sub % per_box == 0;
+                    if (mine_now) sc[stage * 4 + sub] = mine;
+                    const int boxes = __popc(__ballot_sync(0xffffffffu, copy));
+                    // every lane's scales are written before lane 0 arrives
+                    __syncwarp();
+                    if (lane == 0) mbar_expect_tx(full_bar(stage), (uint32_t)(2 * boxes * a.box * D));
+                    __syncwarp();
+                    if (copy) {
+                        const uint32_t dst = sbase + stage * C::STAGE + sub * kSub * D;
+                        tma_load_3d<1>(dst, &map_k, full_bar(stage), 0, y, (int)blk);
+                        tma_load_3d<1>(dst + C::KV, &map_v, full_bar(stage), 0, y, (int)blk);
+                    }
+                    issued |= 1u << stage;
+                    issued_phase = (issued_phase & ~(1u << stage)) | (phase << stage);
+                    if (++stage == kStages) stage = 0, phase ^= 1u;
+                }
+            }
+        }
+        if (!ok)
+            for (int s = 0; s < kStages; ++s)
+                if (issued >> s & 1u) wait_drain(full_bar(s), issued_phase >> s & 1u);
+        return;
+    }
+    // ---------------------------------------------------------- consumers
+    const int g = lane >> 2, c = lane & 3;
+    constexpr int NK = D / 16;  // k-steps of a score
+    constexpr int NV = D / 8;   // 8-wide column tiles of O; also the columns per lane group g
+    float* ml = reinterpret_cast<float*>(smem + C::ML_OFF);  // m [warps][16], l [warps][16]
+    float* osm = reinterpret_cast<float*>(smem + C::O_OFF);
+    volatile int* last_flag = reinterpret_cast<volatile int*>(smem + C::MISC_OFF + 4);
+    for (; w.next(a); w.done()) {
+        const int h = w.item / w.s.rt, rt = w.item - h * w.s.rt;
+        const int rows = w.s.n * a.G;  // rows of the sequence
+        const int r0 = rt * kRows;
+        const int vis_last = w.seen(a, r0 + kRows - 1), vis_first = w.seen(a, r0);
+        const int last = min(w.k1, (vis_last + kTile - 1) / kTile);
+        // q of rows g and g + 8: lane c holds columns [c D/4, (c + 1) D/4), as
+        // the A operand of k-step j the columns 4 j .. 4 j + 3 of those (the
+        // same permutation of the summed axis as K's below)
+        uint32_t qf[NK][4];
+        float crow[2];
+        int vis[2];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            const int r = r0 + g + 8 * x;
+            float v[D / 4];
+#pragma unroll
+            for (int e = 0; e < D / 4; ++e) v[e] = 0.0f;
+            if (r < rows) {
+                const int i = r / a.G;
+                const T* q = static_cast<const T*>(a.Q) + (w.s.lo + i) * a.ldq + (int64_t)(h * a.G + r - i * a.G) * D +
+                             c * (D / 4);
+#pragma unroll
+                for (int e = 0; e < D / 32; ++e) unpack<T>(ldg_nc_v4(q + 8 * e), v + 8 * e);
+            }
+            uint32_t m = 0;
+#pragma unroll
+            for (int e = 0; e < D / 4; ++e) m = max(m, __float_as_uint(v[e]) & 0x7fffffffu);
+            m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+            m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+            const uint32_t field = min(max(m >> 23, 1u), 253u);
+            const float down = __uint_as_float((254u - field) << 23);
+            crow[x] = a.scale * kLog2e * __uint_as_float(field << 23);
+            vis[x] = r < rows ? w.seen(a, r) : 0;
+#pragma unroll
+            for (int j = 0; j < NK; ++j) {
+                qf[j][x] = pack_half2(v[4 * j] * down, v[4 * j + 1] * down);
+                qf[j][2 + x] = pack_half2(v[4 * j + 2] * down, v[4 * j + 3] * down);
+            }
+        }
+        float o[NV][4];
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[j][e] = 0.0f;
+        float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
+        for (int t = w.k0; t < last; ++t) {
+            if (ok) ok = wait_fast(full_bar(stage), phase, abort_flag, a.status, 0x7E2);
+            ok = __all_sync(0xffffffffu, ok);
+            const int key0 = t * kTile + warp * kSub;
+            if (ok && key0 < vis_last) {
+                const float4 sc = reinterpret_cast<const float4*>(smem + C::SC_OFF)[stage * 4 + warp];
+                const uint32_t kb = sbase + stage * C::STAGE + warp * kSub * D, vb = kb + C::KV;
+                float s[2][4];
+#pragma unroll
+                for (int nt = 0; nt < 2; ++nt) {
+                    // K row g of the eight keys: lane c's D / 4 bytes are one
+                    // or two 16-byte units, swizzled by row
+                    const int row = nt * 8 + g;
+                    uint32_t kw[D / 16];
+                    if constexpr (D == 128) {
+                        const uint4 u0 = lds128(kb + row * D + (((2 * c) ^ g) << 4));
+                        const uint4 u1 = lds128(kb + row * D + (((2 * c + 1) ^ g) << 4));
+                        kw[0] = u0.x, kw[1] = u0.y, kw[2] = u0.z, kw[3] = u0.w;
+                        kw[4] = u1.x, kw[5] = u1.y, kw[6] = u1.z, kw[7] = u1.w;
+                    } else {
+                        const uint4 u0 = lds128(kb + row * D + ((c ^ (g >> 1)) << 4));
+                        kw[0] = u0.x, kw[1] = u0.y, kw[2] = u0.z, kw[3] = u0.w;
+                    }
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) s[nt][e] = 0.0f;
+#pragma unroll
+                    for (int j = 0; j < NK; ++j) {
+                        const uint32_t u = kw[j] ^ 0x80808080u;
+                        mma16816(s[nt], qf[j], half2_of(u, 0x4140), half2_of(u, 0x4342));
+                    }
+                }
+                // scores in log2 with the V scale folded in; rows g (x = 0), g + 8
+                const bool masked = key0 + kSub > vis_first;
+                float tm[2];
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const float f = crow[x] * sc.x;
+#pragma unroll
+                    for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            float& v = s[nt][2 * x + e];
+                            v = fmaf(v, f, sc.y);
+                            if (masked && key0 + nt * 8 + 2 * c + e >= vis[x]) v = -INFINITY;
+                        }
+                    float q = fmaxf(fmaxf(s[0][2 * x], s[0][2 * x + 1]), fmaxf(s[1][2 * x], s[1][2 * x + 1]));
+                    q = fmaxf(q, __shfl_xor_sync(0xffffffffu, q, 1));
+                    tm[x] = fmaxf(q, __shfl_xor_sync(0xffffffffu, q, 2));
+                }
+                if (__any_sync(0xffffffffu, tm[0] > m[0] + kSlack || tm[1] > m[1] + kSlack)) {
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        const float to = fmaxf(m[x], tm[x]);
+                        const float f = to == -INFINITY ? 1.0f : ex2(m[x] - to);
+                        m[x] = to;
+                        l[x] *= f;
+#pragma unroll
+                        for (int j = 0; j < NV; ++j) o[j][2 * x] *= f, o[j][2 * x + 1] *= f;
+                    }
+                }
+                uint32_t pf[4];
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const float mu = m[x] == -INFINITY ? 0.0f : m[x];
+                    float sum = 0.0f;
+#pragma unroll
+                    for (int nt = 0; nt < 2; ++nt) {
+                        const float p0 = ex2(s[nt][2 * x] - mu), p1 = ex2(s[nt][2 * x + 1] - mu);
+                        sum += p0 + p1;
+                        pf[nt * 2 + x] = pack_half2(p0, p1);
+                    }
+                    // (a row that sees none of these keys takes nothing from their scale)
+                    if (!masked || key0 < vis[x]) l[x] = fmaf(sum, sc.z, l[x]);
+                }
+                // V: this lane's keys are 2 c, 2 c + 1, 2 c + 8, 2 c + 9, its
+                // columns [g D/8, (g + 1) D/8): column tile j takes column j of
+                // each lane group
+                uint32_t vw[4][D / 32];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int row = 2 * c + (e & 1) + (e >> 1) * 8;
+                    if constexpr (D == 128) {
+                        const uint4 u = lds128(vb + row * D + ((g ^ (row & 7)) << 4));
+                        vw[e][0] = u.x, vw[e][1] = u.y, vw[e][2] = u.z, vw[e][3] = u.w;
+                    } else {
+                        const uint2 u = lds64(vb + row * D + (((g >> 1) ^ ((row >> 1) & 3)) << 4) + (g & 1) * 8);
+                        vw[e][0] = u.x, vw[e][1] = u.y;
+                    }
+                }
+#pragma unroll
+                for (int q = 0; q < D / 32; ++q) {
+                    uint32_t b[2][4];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const uint32_t x0 = vw[2 * e][q] ^ 0x80808080u, x1 = vw[2 * e + 1][q] ^ 0x80808080u;
+                        const uint32_t lo = __byte_perm(x0, x1, 0x5140), hi = __byte_perm(x0, x1, 0x7362);
+                        b[e][0] = half2_of(lo, 0x4140);
+                        b[e][1] = half2_of(lo, 0x4342);
+                        b[e][2] = half2_of(hi, 0x4140);
+                        b[e][3] = half2_of(hi, 0x4342);
+                    }
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) mma16816(o[4 * q + e], pf, b[0][e], b[1][e]);
+                }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(empty_bar(stage));
+            if (++stage == kStages) stage = 0, phase ^= 1u;
+        }
+        // ------------------------------------------------ join the four warps
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            l[x] += __shfl_xor_sync(0xffffffffu, l[x], 1);
+            l[x] += __shfl_xor_sync(0xffffffffu, l[x], 2);
+            if (c == 0) {
+                ml[warp * kRows + g + 8 * x] = m[x];
+                ml[(kCWarps + warp) * kRows + g + 8 * x] = l[x];
+            }
+            float* to = osm + (warp * kRows + g + 8 * x) * C::LDO;
+#pragma unroll
+            for (int y = 0; y < 2; ++y)
+#pragma unroll
+                for (int j = 0; j < NV; j += 4)
+                    *reinterpret_cast<float4*>(to + (2 * c + y) * NV + j) =
+                        make_float4(o[j][2 * x + y], o[j + 1][2 * x + y], o[j + 2][2 * x + y], o[j + 3][2 * x + y]);
+        }
+        asm volatile("bar.sync 1, 128;" ::: "memory");
+        constexpr int CPT = D / 8;  // columns per thread
+        const int row = threadIdx.x >> 3, col = (threadIdx.x & 7) * CPT;
+        float M = -INFINITY, L = 0.0f, acc[CPT];
+#pragma unroll
+        for (int e = 0; e < CPT; ++e) acc[e] = 0.0f;
+#pragma unroll
+        for (int x = 0; x < kCWarps; ++x) M = fmaxf(M, ml[x * kRows + row]);
+#pragma unroll
+        for (int x = 0; x < kCWarps; ++x) {
+            const float mx = ml[x * kRows + row];
+            const float f = mx == -INFINITY ? 0.0f : ex2(mx - M);
+            const float lx = ml[(kCWarps + x) * kRows + row];
+            L += mx == -INFINITY ? lx : lx * f;  // (NaN scores leave m at -inf and l NaN)
+            const float* from = osm + (x * kRows + row) * C::LDO + col;
+#pragma unroll
+            for (int e = 0; e < CPT; ++e) acc[e] = fmaf(from[e], f, acc[e]);
+        }
+        bool write = true;
+        if (w.k0 != 0 || w.k1 != w.s.tiles) {
+            // a part of the row tile's keys: leave it in the workspace; the
+            // block that completes the count joins all parts, in range order
+            constexpr int LDP = D + 2;
+            const int slot = w.first ? 0 : 1;
+            float* mine = a.part + ((int64_t)(blockIdx.x * 2 + slot) * kRows + row) * LDP;
+#pragma unroll
+            for (int e = 0; e < CPT; ++e) __stcg(mine + col + e, acc[e]);
+            if (col == 0) __stcg(mine + D, M), __stcg(mine + D + 1, L);
+            __threadfence();
+            asm volatile("bar.sync 1, 128;" ::: "memory");
+            const int64_t i0 = w.it - w.k0;
+            const int c_lo = w.owner_of(i0), c_hi = w.owner_of(i0 + w.s.tiles - 1);
+            if (threadIdx.x == 0) {
+                const int before = atomicAdd(a.cnt + c_lo, w.k1 - w.k0);
+                const bool is_last = before + (w.k1 - w.k0) == w.s.tiles;
+                if (is_last) a.cnt[c_lo] = 0;  // ready for the next launch
+                *last_flag = is_last;
+            }
+            asm volatile("bar.sync 1, 128;" ::: "memory");
+            write = *last_flag != 0;
+            if (write) {
+                __threadfence();
+                auto part_of = [&](int cc) {
+                    return a.part + ((int64_t)(cc * 2 + (w.start_of(cc) >= i0 ? 0 : 1)) * kRows + row) * LDP;
+                };
+                M = -INFINITY;
+                for (int cc = c_lo; cc <= c_hi; ++cc) M = fmaxf(M, __ldcg(part_of(cc) + D));
+                L = 0.0f;
+#pragma unroll
+                for (int e = 0; e < CPT; ++e) acc[e] = 0.0f;
+                for (int cc = c_lo; cc <= c_hi; ++cc) {
+                    const float* from = part_of(cc);
+                    const float mx = __ldcg(from + D), lx = __ldcg(from + D + 1);
+                    const float f = mx == -INFINITY ? 0.0f : ex2(mx - M);
+                    L += mx == -INFINITY ? lx : lx * f;
+#pragma unroll
+                    for (int e = 0; e < CPT; ++e) acc[e] = fmaf(__ldcg(from + col + e), f, acc[e]);
+                }
+            }
+        }
+        const int r = r0 + row;
+        if (write && r < rows) {
+            const int i = r / a.G;
+            T* y = static_cast<T*>(a.Y) + (w.s.lo + i) * a.ldy + (int64_t)(h * a.G + r - i * a.G) * D + col;
+            // a row that sees no key is zero
+            const float inv = (M == -INFINITY && L == 0.0f) ? 0.0f : __frcp_rn(L);
+            uint32_t p[CPT / 2];
+#pragma unroll
+            for (int e = 0; e < CPT / 2; ++e)
+                p[e] = (uint32_t)to16<T>(acc[2 * e] * inv) | ((uint32_t)to16<T>(acc[2 * e + 1] * inv) << 16);
+#pragma unroll
+            for (int e = 0; e < CPT / 8; ++e)
+                reinterpret_cast<uint4*>(y)[e] = make_uint4(p[4 * e], p[4 * e + 1], p[4 * e + 2], p[4 * e + 3]);
+        }
+        // the next piece writes the shared O and the flag again
+        asm volatile("bar.sync 1, 128;" ::: "memory");
+    }
+}
+
+// The cache as [num_blocks, Hkv * block, D] bytes, box D x box x 1.
+bool make_map_kv(CUtensorMap* m, const int8_t* base, int64_t num_blocks, int64_t rows, int64_t D, int box) {
+    auto fn = encode_fn();
+    if (!fn) return false;
+    cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)rows, (cuuint64_t)num_blocks};
+    cuuint64_t strides[2] = {(cuuint64_t)D, (cuuint64_t)(rows * D)};
+    cuuint32_t bx[3] = {(cuuint32_t)D, (cuuint32_t)box, 1};
+    cuuint32_t estr[3] = {1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<int8_t*>(base), dims, strides, bx, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Counters at a fixed place for every size, one per block of the largest grid.
+constexpr int kMaxGrid = 1024;
+constexpr size_t kCntBytes = kMaxGrid * sizeof(int);
+static_assert(kCntBytes % 256 == 0, "the parts start 256-byte aligned");
+
+int attention_grid() {
+    const int g = kCtasPerSm * num_sms();
+    return g < kMaxGrid ? g : kMaxGrid;
+}
+
+template <typename T, int D>
+sq_status_t launch_attention(const char* name, const CUtensorMap& mk, const CUtensorMap& mv, const AttnArgs& a,
+                             cudaStream_t stream) {
+    auto fn = kv8_attention_kernel<T, D>;
+    if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)ACfg<D>::SMEM_ALLOC) != cudaSuccess)
+        return check_launch(name);
+    launch_pdl(fn, dim3(attention_grid()), dim3(kThreadsA), ACfg<D>::SMEM_ALLOC, stream, mk, mv, a);
+    return check_launch(name);
+}
+
+}  // namespace
+
+size_t kv8_attention_workspace_bytes(int64_t T, int64_t Hq, int64_t D) {
+    if (T <= 0 || Hq <= 0 || D <= 0) return kStatusBytes;
+    return kStatusBytes + kCntBytes + (size_t)attention_grid() * 2 * kRows * (size_t)(D + 2) * sizeof(float);
+}
+
+}  // namespace sq
+
+extern "C" sq_status_t sq_kv8_attention(const void* Q, sq_dtype_t dt, int64_t T, int64_t Hq, int64_t Hkv, int64_t D,
+                                        int64_t ldq, const int8_t* Kc, const int8_t* Vc, const float* kqs,
+                                        const float* vqs, int64_t num_blocks, int64_t block, const int32_t* cu_q,
+                                        const int32_t* seq_lens, int64_t B, const int32_t* block_table,
+                                        int64_t max_blocks, int64_t ldb, float scale, int causal, int64_t max_q, void* Y,
+                                        int64_t ldy, void* workspace, size_t ws_bytes, sq_stream_t stream) {
+    const char* name = "sq_kv8_attention";
+    SQ_REQUIRE(dt == SQ_F16 || dt == SQ_BF16, SQ_ERR_INVALID_ARG, "%s: dtype must be F16 or BF16", name);
+    const sq_status_t st = sq::check_kv8(name, T, B, Hkv, D, block, num_blocks, max_blocks, ldb);
+    if (st != SQ_OK) return st;
+    SQ_REQUIRE(Hq > 0 && Hq % Hkv == 0 && Hq <= 65535, SQ_ERR_UNSUPPORTED_SHAPE,
+               "%s: Hq must be a multiple of Hkv", name);
+    SQ_REQUIRE(ldq >= Hq * D && ldy >= Hq * D, SQ_ERR_UNSUPPORTED_SHAPE, "%s: token strides must be >= Hq * D", name);
+    SQ_REQUIRE(T * (Hq / Hkv) < (1ll << 31) - 16 && Hkv * block < (1ll << 31), SQ_ERR_UNSUPPORTED_SHAPE,
+               "%s: too many rows", name);
+    SQ_REQUIRE(max_q >= 0, SQ_ERR_INVALID_ARG, "%s: max_q must be >= 0", name);
+    if (T == 0 || B == 0) return SQ_OK;
+    SQ_REQUIRE(Q && Kc && Vc && kqs && vqs && cu_q && seq_lens && block_table && Y, SQ_ERR_INVALID_ARG,
+               "%s: null pointer", name);
+    SQ_REQUIRE(sq::aligned16(Q) && sq::aligned16(Y) && sq::aligned16(Kc) && sq::aligned16(Vc) && ldq % 8 == 0 &&
+                   ldy % 8 == 0,
+               SQ_ERR_ALIGNMENT, "%s: Q, Y, the caches and token strides must be 16-byte aligned", name);
+    SQ_REQUIRE(workspace && ws_bytes >= sq::kv8_attention_workspace_bytes(T, Hq, D), SQ_ERR_INVALID_ARG,
+               "%s: needs a workspace of %zu bytes", name, sq::kv8_attention_workspace_bytes(T, Hq, D));
+    sq::AttnArgs a;
+    memset(&a, 0, sizeof(a));
+    a.Q = Q;
+    a.Y = Y;
+    a.ldq = ldq;
+    a.ldy = ldy;
+    a.T = T;
+    a.ldb = ldb;
+    a.num_blocks = num_blocks;
+    a.cu = cu_q;
+    a.lens = seq_lens;
+    a.table = block_table;
+    a.kqs = kqs;
+    a.vqs = vqs;
+    a.B = (int)B;
+    a.Hkv = (int)Hkv;
+    a.G = (int)(Hq / Hkv);
+    a.block = (int)block;
+    a.box = (int)(block < sq::kTile ? block : sq::kTile);
+    a.max_blocks = (int)max_blocks;
+    a.causal = causal != 0;
+    a.scale = scale;
+    a.status = static_cast<int*>(workspace);
+    a.cnt = reinterpret_cast<int*>(static_cast<uint8_t*>(workspace) + sq::kStatusBytes);
+    a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + sq::kStatusBytes + sq::kCntBytes);
+    CUtensorMap mk, mv;
+    if (!sq::make_map_kv(&mk, Kc, num_blocks, Hkv * block, D, a.box) ||
+        !sq::make_map_kv(&mv, Vc, num_blocks, Hkv * block, D, a.box))
+        return sq::set_error(SQ_ERR_CUDA, "%s: cuTensorMapEncodeTiled failed", name);
+    cudaStream_t s = sq::as_cuda(stream);
+    if (dt == SQ_BF16)
+        return D == 128 ? sq::launch_attention<__nv_bfloat16, 128>(name, mk, mv, a, s)
+                        : sq::launch_attention<__nv_bfloat16, 64>(name, mk, mv, a, s);
+    return D == 128 ? sq::launch_attention<__half, 128>(name, mk, mv, a, s)
+                    : sq::launch_attention<__half, 64>(name, mk, mv, a, s);
+}

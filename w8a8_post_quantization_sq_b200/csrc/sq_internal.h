@@ -16,6 +16,8 @@ constexpr size_t kStatusBytes = 256;
 constexpr int kDetectRows = 128;
 size_t detect_workspace_bytes(int64_t M, int64_t K);
 size_t llmint8_workspace_bytes(int64_t M, int64_t N, int64_t K);
+size_t gemm_fp4_workspace_bytes(int64_t M, int64_t N, int64_t K);
+size_t kv8_attention_workspace_bytes(int64_t T, int64_t Hq, int64_t D);
 
 // Outlier counts up to this size use compact fp32 copies of the outlier
 // columns (X_O [M, cap], W_O [cap, N padded to 256]) built in the workspace;

@@ -66,6 +66,8 @@ size_t sq_workspace_size(sq_op_t op, int64_t M, int64_t N, int64_t K) {
         case SQ_OP_QUANT_WEIGHT: return sq::kStatusBytes;
         case SQ_OP_LLMINT8_DETECT: return sq::detect_workspace_bytes(M, K);
         case SQ_OP_LLMINT8: return sq::llmint8_workspace_bytes(M, N, K);
+        case SQ_OP_GEMM_FP4: return sq::gemm_fp4_workspace_bytes(M, N, K);
+        case SQ_OP_KV8_ATTENTION: return sq::kv8_attention_workspace_bytes(M, N, K);
     }
     return 0;
 }
