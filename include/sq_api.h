@@ -451,8 +451,8 @@ SQ_API sq_status_t sq_gemm_fp4(const uint8_t* Xq, const uint8_t* Xs, const uint8
  *   D is 64 or 128; block 16, 32, 64 or 128. All of these are device pointers.
  * sq_kv8_append: writes the new tokens' K and V. For block and head, with `kept`
  *   tokens of the sequence in the block before the call and a = max|x| over the
- *   new tokens that enter it:  qs' = 127 / max(a, 1e-8), and where kept > 0
- *   min(qs, that); new codes clip(rne(x * qs'), -127, 127); where kept > 0 and
+ *   new tokens that enter it:  qs' = fl(127 * fl(1 / max(a, 1e-8))), and where kept >
+ *   0 min(qs, that); new codes clip(rne(x * qs'), -127, 127); where kept > 0 and
  *   qs' < qs the kept codes become clip(rne(code * fl(qs' / qs)), -127, 127).
  *   With kept = 0 what the block and its scales held before is not looked at. A
  *   NaN or an infinity in x makes the scale NaN, and so every row that reads the

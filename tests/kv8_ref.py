@@ -45,7 +45,7 @@ def append_one(x, codes, qs, b, length, batch):
         part = x[done : done + take]
         for h in range(batch.heads):
             rows = part[:, h]
-            now = f32(127.0 / np.maximum(np.abs(rows).max(), f32(1e-8))) if np.isfinite(rows).all() else np.nan
+            now = f32(127.0 * f32(1.0 / np.maximum(np.abs(rows).max(), f32(1e-8)))) if np.isfinite(rows).all() else np.nan
             old = qs[blk, h]
             if kept:
                 now = np.nan if np.isnan(old) else (now if np.isnan(now) else min(now, old))

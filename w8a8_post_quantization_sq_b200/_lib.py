@@ -111,19 +111,27 @@ def _check(name, status):
         raise SqError(name, status, lib().sq_last_error_string().decode())
 
 
+# the current device and its current stream, without building torch objects:
+# a call of a small kernel takes longer to make than to run, and every pointer
+# of every call is checked
+_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                      lambda device: torch.cuda.current_stream(device).cuda_stream)
+
+
 def _ptr(t):
     if t is None:
         return None
-    if not t.is_cuda:
+    d = t.get_device() if t.is_cuda else -1
+    if d < 0:
         raise ValueError("tensor must be on a CUDA device")
-    if t.device.index is not None and t.device.index != torch.cuda.current_device():
-        raise ValueError(f"tensor on {t.device}, but the current device is cuda:{torch.cuda.current_device()}")
-    return ctypes.c_void_p(t.data_ptr())
+    if d != _device():
+        raise ValueError(f"tensor on {t.device}, but the current device is cuda:{_device()}")
+    return t.data_ptr()
 
 
 def _stream(stream):
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return ctypes.c_void_p(s.cuda_stream)
+    return stream.cuda_stream if stream is not None else _raw_stream(_device())
 
 
 def _dt(t):
@@ -475,13 +483,14 @@ def fp4_buffers(rows, K, fmt, device=None):
 
 
 def _fp4(codes, scales, fmt, rows, K, what):
-    _need(fmt in (SQ_NVFP4, SQ_MXFP4), f"unknown format {fmt}")
-    _need(codes.dtype == torch.uint8 and codes.is_contiguous() and tuple(codes.shape) == (rows, K // 2),
-          f"{what}: codes must be contiguous uint8 [{rows}, {K // 2}]")
-    block = 16 if fmt == SQ_NVFP4 else 32
-    need = (rows + 127) // 128 * ((K + 4 * block - 1) // (4 * block)) * 512
-    _need(scales.dtype == torch.uint8 and scales.is_contiguous() and scales.numel() >= need,
-          f"{what}: block scales must be contiguous uint8 of at least {need} bytes")
+    if fmt not in (SQ_NVFP4, SQ_MXFP4):
+        raise ValueError(f"unknown format {fmt}")
+    if codes.dtype != torch.uint8 or not codes.is_contiguous() or codes.shape != (rows, K // 2):
+        raise ValueError(f"{what}: codes must be contiguous uint8 [{rows}, {K // 2}]")
+    span = 64 if fmt == SQ_NVFP4 else 128  # elements per tile of four blocks
+    need = (rows + 127) // 128 * ((K + span - 1) // span) * 512
+    if scales.dtype != torch.uint8 or not scales.is_contiguous() or scales.numel() < need:
+        raise ValueError(f"{what}: block scales must be contiguous uint8 of at least {need} bytes")
 
 
 def sq_quantize_weight_fp4(W, s, fmt, Wq, Ws, qs_w, stream=None):
@@ -536,43 +545,48 @@ def kv8_cache(num_blocks, heads, block, D, device=None):
 
 
 def _kv8(Kc, Vc, kqs, vqs, cu_q, seq_lens, block_table):
-    nb, heads = Kc.shape[:2]
-    _need(Kc.dtype == torch.int8 and Vc.dtype == torch.int8 and Kc.dim() == 4 and Kc.shape == Vc.shape and
-          Kc.is_contiguous() and Vc.is_contiguous(), "Kc and Vc must be contiguous int8 [num_blocks, Hkv, block, D]")
-    _need(tuple(kqs.shape) == (nb, heads) and tuple(vqs.shape) == (nb, heads), "kqs and vqs must be [num_blocks, Hkv]")
+    if (Kc.dtype != torch.int8 or Vc.dtype != torch.int8 or Kc.dim() != 4 or Kc.shape != Vc.shape or
+            not Kc.is_contiguous() or not Vc.is_contiguous()):
+        raise ValueError("Kc and Vc must be contiguous int8 [num_blocks, Hkv, block, D]")
+    if kqs.shape != Kc.shape[:2] or vqs.shape != Kc.shape[:2]:
+        raise ValueError("kqs and vqs must be [num_blocks, Hkv]")
     B = seq_lens.numel()
-    _need(block_table.dim() == 2 and block_table.dtype == torch.int32 and block_table.shape[0] == B and
-          block_table.stride(1) == 1, f"block_table must be int32 [{B}, max_blocks] with unit inner stride")
+    if (block_table.dim() != 2 or block_table.dtype != torch.int32 or block_table.shape[0] != B or
+            block_table.stride(1) != 1 and block_table.shape[1] > 1):
+        raise ValueError(f"block_table must be int32 [{B}, max_blocks] with unit inner stride")
     return (_vec(kqs, torch.float32), _vec(vqs, torch.float32), _vec(cu_q, torch.int32, B + 1),
-            _vec(seq_lens, torch.int32), B)
+            _vec(seq_lens, torch.int32), B, _ptr(block_table), block_table.shape[1],
+            max(block_table.stride(0), block_table.shape[1]) if B < 2 else block_table.stride(0))
 
 
 def _heads(t, what):
-    """[T, heads, D] with heads back to back: its token stride."""
-    _need(t.dim() == 3 and t.stride(2) == 1 and t.stride(1) == t.shape[2],
-          f"{what} must be [T, heads, D] with each token's heads back to back")
-    return t.stride(0)
+    """Token stride of [T, heads, D] whose heads lie back to back (a single token's stride says nothing)."""
+    T, heads, D = t.shape
+    if t.stride(2) != 1 or heads > 1 and t.stride(1) != D:
+        raise ValueError(f"{what} must be [T, heads, D] with each token's heads back to back")
+    return t.stride(0) if T > 1 else heads * D
 
 
 def sq_kv8_append(Kn, Vn, cu_q, seq_lens, block_table, Kc, Vc, kqs, vqs, stream=None):
     """Kn, Vn [T, Hkv, D] (token stride free) into the cache; seq_lens counts the new tokens."""
-    ks, vs, cu, lens, B = _kv8(Kc, Vc, kqs, vqs, cu_q, seq_lens, block_table)
+    ks, vs, cu, lens, B, table, max_blocks, ldb = _kv8(Kc, Vc, kqs, vqs, cu_q, seq_lens, block_table)
+    _need(Kn.dim() == 3 and Vn.shape == Kn.shape and Vn.dtype == Kn.dtype, "Kn and Vn must have one shape and dtype")
     T, heads, D = Kn.shape
-    _need(Vn.shape == Kn.shape and Vn.dtype == Kn.dtype, "Kn and Vn must have one shape and dtype")
-    _need(heads == Kc.shape[1] and D == Kc.shape[3], "Kn and the cache must have the same heads and head width")
+    num_blocks, cache_heads, block, width = Kc.shape
+    _need(heads == cache_heads and D == width, "Kn and the cache must have the same heads and head width")
     _check("sq_kv8_append", lib().sq_kv8_append(
-        _ptr(Kn), _ptr(Vn), _dt(Kn), T, heads, D, _heads(Kn, "Kn"), _heads(Vn, "Vn"), cu, lens, B, _ptr(block_table),
-        block_table.shape[1], block_table.stride(0), _ptr(Kc), _ptr(Vc), ks, vs, Kc.shape[0], Kc.shape[2],
-        _stream(stream)))
+        _ptr(Kn), _ptr(Vn), _dt(Kn), T, heads, D, _heads(Kn, "Kn"), _heads(Vn, "Vn"), cu, lens, B, table, max_blocks,
+        ldb, _ptr(Kc), _ptr(Vc), ks, vs, num_blocks, block, _stream(stream)))
 
 
 def sq_kv8_attention(Q, Kc, Vc, kqs, vqs, cu_q, seq_lens, block_table, scale, causal, max_q, Y, ws, stream=None):
     """Q, Y [T, Hq, D] (token strides free); max_q: the largest number of new tokens of a sequence."""
-    ks, vs, cu, lens, B = _kv8(Kc, Vc, kqs, vqs, cu_q, seq_lens, block_table)
+    ks, vs, cu, lens, B, table, max_blocks, ldb = _kv8(Kc, Vc, kqs, vqs, cu_q, seq_lens, block_table)
+    _need(Q.dim() == 3 and Y.shape == Q.shape and Y.dtype == Q.dtype, "Q and Y must have one shape and dtype")
     T, hq, D = Q.shape
-    _need(Y.shape == Q.shape and Y.dtype == Q.dtype, "Y must have Q's shape and dtype")
-    _need(D == Kc.shape[3], "Q and the cache must have the same head width")
+    num_blocks, heads, block, width = Kc.shape
+    _need(D == width, "Q and the cache must have the same head width")
     _check("sq_kv8_attention", lib().sq_kv8_attention(
-        _ptr(Q), _dt(Q), T, hq, Kc.shape[1], D, _heads(Q, "Q"), _ptr(Kc), _ptr(Vc), ks, vs, Kc.shape[0], Kc.shape[2],
-        cu, lens, B, _ptr(block_table), block_table.shape[1], block_table.stride(0), float(scale), int(causal),
-        int(max_q), _ptr(Y), _heads(Y, "Y"), _ptr(ws), ws.numel(), _stream(stream)))
+        _ptr(Q), _dt(Q), T, hq, heads, D, _heads(Q, "Q"), _ptr(Kc), _ptr(Vc), ks, vs, num_blocks, block, cu, lens, B,
+        table, max_blocks, ldb, float(scale), int(causal), int(max_q), _ptr(Y), _heads(Y, "Y"), _ptr(ws), ws.numel(),
+        _stream(stream)))

@@ -3,7 +3,7 @@
 //
 // For block j of a sequence and head h, with `kept` tokens in it before the
 // call and a = max |x| over the new tokens that enter it:
-//   qs' = 127 / max(a, 1e-8), and min(qs, that) where kept > 0
+//   qs' = fl(127 fl(1 / max(a, 1e-8))), and min(qs, that) where kept > 0
 //   new codes      = rne(x qs') clipped to +-127
 //   codes of kept  = rne(code fl(qs' / qs)) where qs' < qs, else as they were
 // so a block's scale always covers every token in it, and a call that enters a
@@ -86,7 +86,7 @@ __device__ __forceinline__ void fill_block(const T* src, int64_t ld, int nt, int
         }
     }
     const uint32_t m = __reduce_max_sync(0xffffffffu, max(m2 & 0xffffu, m2 >> 16));
-    float now = __fdiv_rn(127.0f, fmaxf(from_bits16<T>(m), 1e-8f));
+    float now = __fmul_rn(127.0f, __frcp_rn(fmaxf(from_bits16<T>(m), 1e-8f)));
     if (m >= kInf16 || (kept > 0 && old != old)) now = __uint_as_float(0x7fffffffu);
     else if (kept > 0) now = fminf(now, old);
     if (kept > 0 && now < old) rescale(codes, kept * D, __fdiv_rn(now, old), lane);
