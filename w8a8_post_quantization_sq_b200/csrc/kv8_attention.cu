@@ -21,15 +21,17 @@
 // lose bits that the fp32 sum could not hold either).
 //
 // Work: rows (new token, query head of the group) of one sequence and K/V head
-// make row tiles of 16; the keys of each row tile are cut into tiles of 64, and
-// the list of all tiles is cut into one contiguous range per block (the lengths
-// are on the device; every block works out its own range). A row tile whose
-// keys fall into several ranges is joined by the block that finishes last,
+// make row tiles of 8 or 16; the keys of each row tile are cut into tiles of 64,
+// and the list of all tiles is cut into one contiguous range per block (the
+// lengths are on the device; every block works out its own range). A row tile
+// whose keys fall into several ranges is joined by the block that finishes last,
 // in range order, so results do not depend on timing.
 // In a block, one warp brings 64 keys' K and V by TMA (swizzled, ring of
-// stages), and four warps take 16 keys each; scores and outputs are
-// mma.m16n8k16 (a decode step has 1 to 16 rows per K/V head, an eighth of the
-// smallest tcgen05 tile, and is bound by the cache's bytes).
+// stages), and four warps take 16 keys each. A decode step has 1 to 16 rows per
+// K/V head, an eighth of the smallest tcgen05 tile, and is bound by the cache's
+// bytes and by the conversions, so the products are mma.m16n8k16 with the keys
+// (K) and the columns (V) on the 16-wide side and 8 rows on the other: half the
+// instructions and registers of the usual orientation.
 #include <cstring>
 
 #include "sq_internal.h"
@@ -47,11 +49,11 @@ constexpr int kTile = 64;     // keys per stage
 constexpr int kSub = 16;      // keys per warp of a stage
 constexpr int kCWarps = 4;    // consumer warps
 constexpr int kThreadsA = 32 * (kCWarps + 1);
-constexpr int kStages = 4;
-constexpr int kRows = 16;
+constexpr int kStages = 3;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kSlack = 8.0f;
-constexpr int kCtasPerSm = 2;
+// blocks per SM by row groups of 8: registers (accumulators) and shared memory
+constexpr int ctas_per_sm(int nr) { return nr == 1 ? 3 : 2; }
 
 struct AttnArgs {
     const void* Q;
@@ -66,20 +68,21 @@ struct AttnArgs {
     float scale;
     int* status;
     int* cnt;     // [grid] key tiles counted in per row tile (zero between launches)
-    float* part;  // [grid][2][16][D + 2]: O, then m and l
+    float* part;  // [grid][2]: O [rows][D], m [rows], l [rows]
 };
 
-template <int D>
+template <int D, int NR>
 struct ACfg {
+    static constexpr int ROWS = 8 * NR;
     static constexpr uint32_t KV = kTile * D;  // bytes of one stage's K (and of its V)
     static constexpr uint32_t STAGE = 2 * KV;
     static constexpr uint32_t SC_OFF = kStages * STAGE;              // float4 [stages][4]: 1/kqs, -log2 vqs, vqs
     static constexpr uint32_t BAR_OFF = SC_OFF + kStages * 4 * 16;   // full[S], empty[S]
     static constexpr uint32_t MISC_OFF = BAR_OFF + 2 * kStages * 8;  // abort flag, last flag
-    static constexpr uint32_t ML_OFF = MISC_OFF + 16;                // m, l [warps][16]
+    static constexpr uint32_t ML_OFF = MISC_OFF + 16;                // m, l [warps][rows]
     static constexpr int LDO = D + 4;                                // floats per row of a warp's O
-    static constexpr uint32_t O_OFF = ML_OFF + kCWarps * kRows * 2 * 4;
-    static constexpr uint32_t SMEM = O_OFF + kCWarps * kRows * LDO * 4;
+    static constexpr uint32_t O_OFF = ML_OFF + kCWarps * ROWS * 2 * 4;
+    static constexpr uint32_t SMEM = O_OFF + kCWarps * ROWS * LDO * 4;
     static constexpr uint32_t SMEM_ALLOC = SMEM + 1024;
 };
 
@@ -118,12 +121,20 @@ __device__ __forceinline__ uint32_t pack_half2(float a, float b) {
     return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+// An 8 x 8 tile of 16-bit elements transposed across the warp.
+__device__ __forceinline__ uint32_t movmatrix(uint32_t v) {
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    return r;
+}
+
 // One sequence's share of the work.
 struct Seq {
     int64_t lo;  // first new token
     int n, len, rt, tiles;
     __device__ int64_t work(int Hkv) const { return (int64_t)Hkv * rt * tiles; }
 };
+template <int ROWS>
 __device__ __forceinline__ Seq seq_of(const AttnArgs& a, int b) {
     Seq s;
     const int64_t lo = min(max((int64_t)__ldg(a.cu + b), (int64_t)0), a.T);
@@ -131,13 +142,14 @@ __device__ __forceinline__ Seq seq_of(const AttnArgs& a, int b) {
     s.lo = lo;
     s.n = (int)max(hi - lo, (int64_t)0);
     s.len = min(max(__ldg(a.lens + b), 0), a.max_blocks * a.block);
-    s.rt = (int)(((int64_t)s.n * a.G + kRows - 1) / kRows);
+    s.rt = (int)(((int64_t)s.n * a.G + ROWS - 1) / ROWS);
     s.tiles = max((s.len + kTile - 1) / kTile, 1);  // a sequence without keys still has rows to write
     return s;
 }
 
 // A block's range of the list of key tiles, as pieces: the part of the range
 // inside one row tile. Every warp walks the same sequence.
+template <int ROWS>
 struct Walk {
     int64_t it, end, total, units;
     int b, item, k0, k1;
@@ -148,7 +160,7 @@ struct Walk {
 
     __device__ __forceinline__ void init(const AttnArgs& a, int lane) {
         int64_t sum = 0;
-        for (int i = lane; i < a.B; i += 32) sum += seq_of(a, i).work(a.Hkv);
+        for (int i = lane; i < a.B; i += 32) sum += seq_of<ROWS>(a, i).work(a.Hkv);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
         total = sum;
@@ -162,7 +174,7 @@ struct Walk {
         // the sequence that holds `it`
         int64_t before = 0;
         for (int base = 0; base < a.B; base += 32) {
-            const int64_t w = base + lane < a.B ? seq_of(a, base + lane).work(a.Hkv) : 0;
+            const int64_t w = base + lane < a.B ? seq_of<ROWS>(a, base + lane).work(a.Hkv) : 0;
             int64_t inc = w;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -178,7 +190,7 @@ struct Walk {
             }
             before += __shfl_sync(0xffffffffu, inc, 31);
         }
-        s = seq_of(a, b);
+        s = seq_of<ROWS>(a, b);
         const int64_t r = it - before;
         item = (int)(r / s.tiles);
         k0 = (int)(r - (int64_t)item * s.tiles);
@@ -187,7 +199,7 @@ struct Walk {
     __device__ __forceinline__ bool next(const AttnArgs& a) {
         if (it >= end) return false;
         while (item >= a.Hkv * s.rt) {
-            s = seq_of(a, ++b);
+            s = seq_of<ROWS>(a, ++b);
             item = 0;
         }
         k1 = (int)min((int64_t)s.tiles, k0 + (end - it));
@@ -206,11 +218,12 @@ struct Walk {
     }
 };
 
-template <typename T, int D>
-__global__ void __launch_bounds__(kThreadsA, kCtasPerSm)
+template <typename T, int D, int NR>
+__global__ void __launch_bounds__(kThreadsA, ctas_per_sm(NR))
 kv8_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
                      const AttnArgs a) {
-    using C = ACfg<D>;
+    using C = ACfg<D, NR>;
+    constexpr int ROWS = C::ROWS;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t sbase = smem_u32(smem);
@@ -230,7 +243,7 @@ kv8_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
     __syncthreads();
     pdl_wait();
     pdl_trigger();
-    Walk w;
+    Walk<ROWS> w;
     w.init(a, lane);
     int stage = 0;
     uint32_t phase = 0;
@@ -242,24 +255,25 @@ kv8_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
         uint32_t issued = 0, issued_phase = 0;
         for (; ok && w.next(a); w.done()) {
             const int h = w.item / w.s.rt, rt = w.item - h * w.s.rt;
-            const int vis = w.seen(a, rt * kRows + kRows - 1);
+            const int vis = w.seen(a, rt * ROWS + ROWS - 1);
             const int last = min(w.k1, (vis + kTile - 1) / kTile);
             const int32_t* row = a.table + (int64_t)w.b * a.ldb;
-            // lane l looks after part l of eight tiles' 32 parts
+            // lane l looks after part l of eight tiles' 32 parts; the next
+            // eight tiles' block numbers are on their way meanwhile
+            auto block_of = [&](int t0) {
+                const int key = t0 * kTile + lane * kSub;
+                return key < vis ? __ldg(row + key / a.block) : -1;
+            };
+            int blk_next = block_of(w.k0);
             for (int t0 = w.k0; ok && t0 < last; t0 += 8) {
                 const int key = t0 * kTile + lane * kSub;
-                int64_t blk = -1;
-                float kq = __uint_as_float(0x7fffffffu), vq = kq;
-                if (key < vis) {
-                    blk = __ldg(row + key / a.block);
-                    if (blk >= 0 && blk < a.num_blocks) {
-                        kq = __ldg(a.kqs + blk * a.Hkv + h);
-                        vq = __ldg(a.vqs + blk * a.Hkv + h);
-                    } else {
-                        blk = -1;  // no such block: NaN scales, nothing read
-                    }
+                const int64_t blk = blk_next >= 0 && blk_next < a.num_blocks ? blk_next : -1;
+                float kq = __uint_as_float(0x7fffffffu), vq = kq;  // no such block: NaN scales, nothing read
+                if (blk >= 0) {
+                    kq = __ldg(a.kqs + blk * a.Hkv + h);
+                    vq = __ldg(a.vqs + blk * a.Hkv + h);
                 }
-                const float4 mine = make_float4(__frcp_rn(kq), -__log2f(vq), vq, 0.0f);
+                if (t0 + 8 < last) blk_next = block_of(t0 + 8);
                 const int y = h * a.block + (key & (a.block - 1));
                 for (int t = t0; t < min(t0 + 8, last); ++t) {
                     ok = wait_fast(empty_bar(stage), phase ^ 1u, abort_flag, a.status, 0x7E1);
@@ -270,17 +284,18 @@ kv8_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
                     const int sub = lane - (t - t0) * 4;
                     const bool mine_now = sub >= 0 && sub < 4;
                     const bool copy = mine_now && blk >= 0 && sub % per_box == 0;
-                    if (mine_now) sc[stage * 4 + sub] = mine;
                     const int boxes = __popc(__ballot_sync(0xffffffffu, copy));
-                    // every lane's scales are written before lane 0 arrives
-                    __syncwarp();
-                    if (lane == 0) mbar_expect_tx(full_bar(stage), (uint32_t)(2 * boxes * a.box * D));
+                    if (lane == 0) mbar_expect_tx_only(full_bar(stage), (uint32_t)(2 * boxes * a.box * D));
                     __syncwarp();
                     if (copy) {
                         const uint32_t dst = sbase + stage * C::STAGE + sub * kSub * D;
                         tma_load_3d<1>(dst, &map_k, full_bar(stage), 0, y, (int)blk);
                         tma_load_3d<1>(dst + C::KV, &map_v, full_bar(stage), 0, y, (int)blk);
                     }
+                    // the scales arrive while the copies run
+                    if (mine_now) sc[stage * 4 + sub] = make_float4(__frcp_rn(kq), -__log2f(vq), vq, 0.0f);
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(full_bar(stage));
                     issued |= 1u << stage;
                     issued_phase = (issued_phase & ~(1u << stage)) | (phase << stage);
                     if (++stage == kStages) stage = 0, phase ^= 1u;
@@ -295,25 +310,26 @@ kv8_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
     // ---------------------------------------------------------- consumers
     const int g = lane >> 2, c = lane & 3;
     constexpr int NK = D / 16;  // k-steps of a score
-    constexpr int NV = D / 8;   // 8-wide column tiles of O; also the columns per lane group g
-    float* ml = reinterpret_cast<float*>(smem + C::ML_OFF);  // m [warps][16], l [warps][16]
+    constexpr int NO = D / 16;  // 16-column tiles of O
+    constexpr int DG = D / 8;   // columns of O per lane group g
+    float* ml = reinterpret_cast<float*>(smem + C::ML_OFF);  // m [warps][rows], l [warps][rows]
     float* osm = reinterpret_cast<float*>(smem + C::O_OFF);
     volatile int* last_flag = reinterpret_cast<volatile int*>(smem + C::MISC_OFF + 4);
     for (; w.next(a); w.done()) {
         const int h = w.item / w.s.rt, rt = w.item - h * w.s.rt;
         const int rows = w.s.n * a.G;  // rows of the sequence
-        const int r0 = rt * kRows;
-        const int vis_last = w.seen(a, r0 + kRows - 1), vis_first = w.seen(a, r0);
+        const int r0 = rt * ROWS;
+        const int vis_last = w.seen(a, r0 + ROWS - 1), vis_first = w.seen(a, r0);
         const int last = min(w.k1, (vis_last + kTile - 1) / kTile);
-        // q of rows g and g + 8: lane c holds columns [c D/4, (c + 1) D/4), as
-        // the A operand of k-step j the columns 4 j .. 4 j + 3 of those (the
-        // same permutation of the summed axis as K's below)
-        uint32_t qf[NK][4];
-        float crow[2];
-        int vis[2];
+        // q of row g of each group of 8: lane c holds columns [c D/4, (c + 1)
+        // D/4), as the B operand of k-step j the columns 4 j .. 4 j + 3 of those
+        // (the same permutation of the summed axis as K's below)
+        uint32_t qf[NR][NK][2];
+        float crow[NR][2];  // of this lane's rows 2 c, 2 c + 1: score of the codes -> log2
+        int vis[NR][2];
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-            const int r = r0 + g + 8 * x;
+        for (int z = 0; z < NR; ++z) {
+            const int r = r0 + 8 * z + g;
             float v[D / 4];
 #pragma unroll
             for (int e = 0; e < D / 4; ++e) v[e] = 0.0f;
@@ -331,20 +347,32 @@ kv8_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
             m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
             const uint32_t field = min(max(m >> 23, 1u), 253u);
             const float down = __uint_as_float((254u - field) << 23);
-            crow[x] = a.scale * kLog2e * __uint_as_float(field << 23);
-            vis[x] = r < rows ? w.seen(a, r) : 0;
+            const float cr = a.scale * kLog2e * __uint_as_float(field << 23);
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                crow[z][x] = __shfl_sync(0xffffffffu, cr, (2 * c + x) * 4);
+                const int rr = r0 + 8 * z + 2 * c + x;
+                vis[z][x] = rr < rows ? w.seen(a, rr) : 0;
+            }
 #pragma unroll
             for (int j = 0; j < NK; ++j) {
-                qf[j][x] = pack_half2(v[4 * j] * down, v[4 * j + 1] * down);
-                qf[j][2 + x] = pack_half2(v[4 * j + 2] * down, v[4 * j + 3] * down);
+                qf[z][j][0] = pack_half2(v[4 * j] * down, v[4 * j + 1] * down);
+                qf[z][j][1] = pack_half2(v[4 * j + 2] * down, v[4 * j + 3] * down);
             }
         }
-        float o[NV][4];
+        // O transposed: tile j holds columns g DG + 2 j (elements 0, 1: rows 2 c,
+        // 2 c + 1) and g DG + 2 j + 1 (elements 2, 3)
+        float o[NR][NO][4];
+        float m[NR][2], l[NR][2];
 #pragma unroll
-        for (int j = 0; j < NV; ++j)
+        for (int z = 0; z < NR; ++z) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) o[j][e] = 0.0f;
-        float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
+            for (int j = 0; j < NO; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[z][j][e] = 0.0f;
+            m[z][0] = m[z][1] = -INFINITY;
+            l[z][0] = l[z][1] = 0.0f;
+        }
         for (int t = w.k0; t < last; ++t) {
             if (ok) ok = wait_fast(full_bar(stage), phase, abort_flag, a.status, 0x7E2);
             ok = __all_sync(0xffffffffu, ok);
@@ -352,76 +380,24 @@ kv8_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
             if (ok && key0 < vis_last) {
                 const float4 sc = reinterpret_cast<const float4*>(smem + C::SC_OFF)[stage * 4 + warp];
                 const uint32_t kb = sbase + stage * C::STAGE + warp * kSub * D, vb = kb + C::KV;
-                float s[2][4];
+                // keys g and g + 8: lane c's D / 4 bytes are one or two 16-byte
+                // units, swizzled by row
+                uint32_t kw[2][D / 16];
 #pragma unroll
-                for (int nt = 0; nt < 2; ++nt) {
-                    // K row g of the eight keys: lane c's D / 4 bytes are one
-                    // or two 16-byte units, swizzled by row
-                    const int row = nt * 8 + g;
-                    uint32_t kw[D / 16];
+                for (int x = 0; x < 2; ++x) {
+                    const int row = g + 8 * x;
                     if constexpr (D == 128) {
                         const uint4 u0 = lds128(kb + row * D + (((2 * c) ^ g) << 4));
                         const uint4 u1 = lds128(kb + row * D + (((2 * c + 1) ^ g) << 4));
-                        kw[0] = u0.x, kw[1] = u0.y, kw[2] = u0.z, kw[3] = u0.w;
-                        kw[4] = u1.x, kw[5] = u1.y, kw[6] = u1.z, kw[7] = u1.w;
+                        kw[x][0] = u0.x, kw[x][1] = u0.y, kw[x][2] = u0.z, kw[x][3] = u0.w;
+                        kw[x][4] = u1.x, kw[x][5] = u1.y, kw[x][6] = u1.z, kw[x][7] = u1.w;
                     } else {
                         const uint4 u0 = lds128(kb + row * D + ((c ^ (g >> 1)) << 4));
-                        kw[0] = u0.x, kw[1] = u0.y, kw[2] = u0.z, kw[3] = u0.w;
+                        kw[x][0] = u0.x, kw[x][1] = u0.y, kw[x][2] = u0.z, kw[x][3] = u0.w;
                     }
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) s[nt][e] = 0.0f;
-#pragma unroll
-                    for (int j = 0; j < NK; ++j) {
-                        const uint32_t u = kw[j] ^ 0x80808080u;
-                        mma16816(s[nt], qf[j], half2_of(u, 0x4140), half2_of(u, 0x4342));
-                    }
-                }
-                // scores in log2 with the V scale folded in; rows g (x = 0), g + 8
-                const bool masked = key0 + kSub > vis_first;
-                float tm[2];
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    const float f = crow[x] * sc.x;
-#pragma unroll
-                    for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            float& v = s[nt][2 * x + e];
-                            v = fmaf(v, f, sc.y);
-                            if (masked && key0 + nt * 8 + 2 * c + e >= vis[x]) v = -INFINITY;
-                        }
-                    float q = fmaxf(fmaxf(s[0][2 * x], s[0][2 * x + 1]), fmaxf(s[1][2 * x], s[1][2 * x + 1]));
-                    q = fmaxf(q, __shfl_xor_sync(0xffffffffu, q, 1));
-                    tm[x] = fmaxf(q, __shfl_xor_sync(0xffffffffu, q, 2));
-                }
-                if (__any_sync(0xffffffffu, tm[0] > m[0] + kSlack || tm[1] > m[1] + kSlack)) {
-#pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        const float to = fmaxf(m[x], tm[x]);
-                        const float f = to == -INFINITY ? 1.0f : ex2(m[x] - to);
-                        m[x] = to;
-                        l[x] *= f;
-#pragma unroll
-                        for (int j = 0; j < NV; ++j) o[j][2 * x] *= f, o[j][2 * x + 1] *= f;
-                    }
-                }
-                uint32_t pf[4];
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    const float mu = m[x] == -INFINITY ? 0.0f : m[x];
-                    float sum = 0.0f;
-#pragma unroll
-                    for (int nt = 0; nt < 2; ++nt) {
-                        const float p0 = ex2(s[nt][2 * x] - mu), p1 = ex2(s[nt][2 * x + 1] - mu);
-                        sum += p0 + p1;
-                        pf[nt * 2 + x] = pack_half2(p0, p1);
-                    }
-                    // (a row that sees none of these keys takes nothing from their scale)
-                    if (!masked || key0 < vis[x]) l[x] = fmaf(sum, sc.z, l[x]);
                 }
                 // V: this lane's keys are 2 c, 2 c + 1, 2 c + 8, 2 c + 9, its
-                // columns [g D/8, (g + 1) D/8): column tile j takes column j of
-                // each lane group
+                // columns [g DG, (g + 1) DG)
                 uint32_t vw[4][D / 32];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
@@ -433,6 +409,69 @@ kv8_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
                         const uint2 u = lds64(vb + row * D + (((g >> 1) ^ ((row >> 1) & 3)) << 4) + (g & 1) * 8);
                         vw[e][0] = u.x, vw[e][1] = u.y;
                     }
+                }
+                float s[NR][4];  // keys g (elements 0, 1), g + 8 (2, 3); rows 2 c, 2 c + 1
+#pragma unroll
+                for (int z = 0; z < NR; ++z)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) s[z][e] = 0.0f;
+#pragma unroll
+                for (int j = 0; j < NK; ++j) {
+                    const uint32_t u0 = kw[0][j] ^ 0x80808080u, u1 = kw[1][j] ^ 0x80808080u;
+                    const uint32_t af[4] = {half2_of(u0, 0x4140), half2_of(u1, 0x4140), half2_of(u0, 0x4342),
+                                            half2_of(u1, 0x4342)};
+#pragma unroll
+                    for (int z = 0; z < NR; ++z) mma16816(s[z], af, qf[z][j][0], qf[z][j][1]);
+                }
+                // scores in log2 with the V scale folded in
+                const bool masked = key0 + kSub > vis_first;
+                float tm[NR][2];
+                bool move = false;
+#pragma unroll
+                for (int z = 0; z < NR; ++z)
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        const float f = crow[z][x] * sc.x;
+                        s[z][x] = fmaf(s[z][x], f, sc.y);
+                        s[z][2 + x] = fmaf(s[z][2 + x], f, sc.y);
+                        if (masked) {
+                            if (key0 + g >= vis[z][x]) s[z][x] = -INFINITY;
+                            if (key0 + g + 8 >= vis[z][x]) s[z][2 + x] = -INFINITY;
+                        }
+                        float q = fmaxf(s[z][x], s[z][2 + x]);
+                        q = fmaxf(q, __shfl_xor_sync(0xffffffffu, q, 4));
+                        q = fmaxf(q, __shfl_xor_sync(0xffffffffu, q, 8));
+                        tm[z][x] = fmaxf(q, __shfl_xor_sync(0xffffffffu, q, 16));
+                        move |= tm[z][x] > m[z][x] + kSlack;
+                    }
+                if (__any_sync(0xffffffffu, move)) {
+#pragma unroll
+                    for (int z = 0; z < NR; ++z)
+#pragma unroll
+                        for (int x = 0; x < 2; ++x) {
+                            const float to = fmaxf(m[z][x], tm[z][x]);
+                            const float f = to == -INFINITY ? 1.0f : ex2(m[z][x] - to);
+                            m[z][x] = to;
+                            l[z][x] *= f;
+#pragma unroll
+                            for (int j = 0; j < NO; ++j) o[z][j][x] *= f, o[z][j][2 + x] *= f;
+                        }
+                }
+                uint32_t pf[NR][2];
+#pragma unroll
+                for (int z = 0; z < NR; ++z) {
+                    float p[4];
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        const float mu = m[z][x] == -INFINITY ? 0.0f : m[z][x];
+                        p[x] = ex2(s[z][x] - mu);
+                        p[2 + x] = ex2(s[z][2 + x] - mu);
+                        // (a row that sees none of these keys takes nothing from their scale)
+                        if (!masked || key0 < vis[z][x]) l[z][x] = fmaf(p[x] + p[2 + x], sc.z, l[z][x]);
+                    }
+                    // rows to the lane groups, keys to the lanes: the B operand
+                    pf[z][0] = movmatrix(pack_half2(p[0], p[1]));
+                    pf[z][1] = movmatrix(pack_half2(p[2], p[3]));
                 }
 #pragma unroll
                 for (int q = 0; q < D / 32; ++q) {
@@ -447,7 +486,11 @@ kv8_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
                         b[e][3] = half2_of(hi, 0x4342);
                     }
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) mma16816(o[4 * q + e], pf, b[0][e], b[1][e]);
+                    for (int e = 0; e < 2; ++e) {
+                        const uint32_t af[4] = {b[0][2 * e], b[0][2 * e + 1], b[1][2 * e], b[1][2 * e + 1]};
+#pragma unroll
+                        for (int z = 0; z < NR; ++z) mma16816(o[z][2 * q + e], af, pf[z][0], pf[z][1]);
+                    }
                 }
             }
             __syncwarp();
@@ -456,36 +499,52 @@ kv8_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
         }
         // ------------------------------------------------ join the four warps
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-            l[x] += __shfl_xor_sync(0xffffffffu, l[x], 1);
-            l[x] += __shfl_xor_sync(0xffffffffu, l[x], 2);
-            if (c == 0) {
-                ml[warp * kRows + g + 8 * x] = m[x];
-                ml[(kCWarps + warp) * kRows + g + 8 * x] = l[x];
+        for (int z = 0; z < NR; ++z)
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                float s = l[z][x];
+                s += __shfl_xor_sync(0xffffffffu, s, 4);
+                s += __shfl_xor_sync(0xffffffffu, s, 8);
+                s += __shfl_xor_sync(0xffffffffu, s, 16);
+                const int row = 8 * z + 2 * c + x;
+                if (g == 0) {
+                    ml[warp * ROWS + row] = m[z][x];
+                    ml[(kCWarps + warp) * ROWS + row] = s;
+                }
+                float* to = osm + (warp * ROWS + row) * C::LDO + g * DG;
+#pragma unroll
+                for (int j = 0; j < NO; j += 2)
+                    *reinterpret_cast<float4*>(to + 2 * j) =
+                        make_float4(o[z][j][x], o[z][j][2 + x], o[z][j + 1][x], o[z][j + 1][2 + x]);
             }
-            float* to = osm + (warp * kRows + g + 8 * x) * C::LDO;
-#pragma unroll
-            for (int y = 0; y < 2; ++y)
-#pragma unroll
-                for (int j = 0; j < NV; j += 4)
-                    *reinterpret_cast<float4*>(to + (2 * c + y) * NV + j) =
-                        make_float4(o[j][2 * x + y], o[j + 1][2 * x + y], o[j + 2][2 * x + y], o[j + 3][2 * x + y]);
-        }
         asm volatile("bar.sync 1, 128;" ::: "memory");
-        constexpr int CPT = D / 8;  // columns per thread
-        const int row = threadIdx.x >> 3, col = (threadIdx.x & 7) * CPT;
+        constexpr int CPT = ROWS * D / 128;  // columns per thread
+        constexpr int TPR = D / CPT;
+        const int row = threadIdx.x / TPR, col = (threadIdx.x % TPR) * CPT;
         float M = -INFINITY, L = 0.0f, acc[CPT];
 #pragma unroll
         for (int e = 0; e < CPT; ++e) acc[e] = 0.0f;
+        // adds another part of the keys (m, l, O) to (M, L, acc); M is final
+        auto add = [&](float mx, float lx, const float* from) {
+            const float f = mx == -INFINITY ? 0.0f : ex2(mx - M);
+            L += mx == -INFINITY ? lx : lx * f;  // (NaN scores leave m at -inf and l NaN)
 #pragma unroll
-        for (int x = 0; x < kCWarps; ++x) M = fmaxf(M, ml[x * kRows + row]);
+            for (int e = 0; e < CPT; e += 4) {
+                const float4 v = __ldcg(reinterpret_cast<const float4*>(from + e));
+                acc[e] = fmaf(v.x, f, acc[e]);
+                acc[e + 1] = fmaf(v.y, f, acc[e + 1]);
+                acc[e + 2] = fmaf(v.z, f, acc[e + 2]);
+                acc[e + 3] = fmaf(v.w, f, acc[e + 3]);
+            }
+        };
+#pragma unroll
+        for (int x = 0; x < kCWarps; ++x) M = fmaxf(M, ml[x * ROWS + row]);
 #pragma unroll
         for (int x = 0; x < kCWarps; ++x) {
-            const float mx = ml[x * kRows + row];
+            const float mx = ml[x * ROWS + row], lx = ml[(kCWarps + x) * ROWS + row];
             const float f = mx == -INFINITY ? 0.0f : ex2(mx - M);
-            const float lx = ml[(kCWarps + x) * kRows + row];
-            L += mx == -INFINITY ? lx : lx * f;  // (NaN scores leave m at -inf and l NaN)
-            const float* from = osm + (x * kRows + row) * C::LDO + col;
+            L += mx == -INFINITY ? lx : lx * f;
+            const float* from = osm + (x * ROWS + row) * C::LDO + col;
 #pragma unroll
             for (int e = 0; e < CPT; ++e) acc[e] = fmaf(from[e], f, acc[e]);
         }
@@ -493,16 +552,20 @@ kv8_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
         if (w.k0 != 0 || w.k1 != w.s.tiles) {
             // a part of the row tile's keys: leave it in the workspace; the
             // block that completes the count joins all parts, in range order
-            constexpr int LDP = D + 2;
-            const int slot = w.first ? 0 : 1;
-            float* mine = a.part + ((int64_t)(blockIdx.x * 2 + slot) * kRows + row) * LDP;
+            constexpr int PART = ROWS * (D + 2);
+            float* mine = a.part + (int64_t)(blockIdx.x * 2 + (w.first ? 0 : 1)) * PART;
 #pragma unroll
-            for (int e = 0; e < CPT; ++e) __stcg(mine + col + e, acc[e]);
-            if (col == 0) __stcg(mine + D, M), __stcg(mine + D + 1, L);
+            for (int e = 0; e < CPT; e += 4)
+                __stcg(reinterpret_cast<float4*>(mine + row * D + col + e),
+                       make_float4(acc[e], acc[e + 1], acc[e + 2], acc[e + 3]));
+            if (col == 0) {
+                __stcg(mine + ROWS * D + row, M);
+                __stcg(mine + ROWS * D + ROWS + row, L);
+            }
             __threadfence();
             asm volatile("bar.sync 1, 128;" ::: "memory");
             const int64_t i0 = w.it - w.k0;
-            const int c_lo = w.owner_of(i0), c_hi = w.owner_of(i0 + w.s.tiles - 1);
+            const int c_lo = w.owner_of(i0);
             if (threadIdx.x == 0) {
                 const int before = atomicAdd(a.cnt + c_lo, w.k1 - w.k0);
                 const bool is_last = before + (w.k1 - w.k0) == w.s.tiles;
@@ -513,21 +576,24 @@ kv8_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
             write = *last_flag != 0;
             if (write) {
                 __threadfence();
-                auto part_of = [&](int cc) {
-                    return a.part + ((int64_t)(cc * 2 + (w.start_of(cc) >= i0 ? 0 : 1)) * kRows + row) * LDP;
-                };
-                M = -INFINITY;
-                for (int cc = c_lo; cc <= c_hi; ++cc) M = fmaxf(M, __ldcg(part_of(cc) + D));
+                const int c_hi = w.owner_of(i0 + w.s.tiles - 1);
+                // the row tile is the last piece of the range it starts in
+                // (unless it starts that range), the first of the later ones
+                const float* p_lo =
+                    a.part + (int64_t)(c_lo * 2 + (w.start_of(c_lo) == i0 ? 0 : 1)) * PART;
+                const float* p_hi = a.part + (int64_t)(c_lo + 1) * 2 * PART;
+                const int more = c_hi - c_lo;
+                M = __ldcg(p_lo + ROWS * D + row);
+#pragma unroll 8
+                for (int x = 0; x < more; ++x) M = fmaxf(M, __ldcg(p_hi + (int64_t)x * 2 * PART + ROWS * D + row));
                 L = 0.0f;
 #pragma unroll
                 for (int e = 0; e < CPT; ++e) acc[e] = 0.0f;
-                for (int cc = c_lo; cc <= c_hi; ++cc) {
-                    const float* from = part_of(cc);
-                    const float mx = __ldcg(from + D), lx = __ldcg(from + D + 1);
-                    const float f = mx == -INFINITY ? 0.0f : ex2(mx - M);
-                    L += mx == -INFINITY ? lx : lx * f;
-#pragma unroll
-                    for (int e = 0; e < CPT; ++e) acc[e] = fmaf(__ldcg(from + col + e), f, acc[e]);
+                add(__ldcg(p_lo + ROWS * D + row), __ldcg(p_lo + ROWS * D + ROWS + row), p_lo + row * D + col);
+#pragma unroll 4
+                for (int x = 0; x < more; ++x) {
+                    const float* p = p_hi + (int64_t)x * 2 * PART;
+                    add(__ldcg(p + ROWS * D + row), __ldcg(p + ROWS * D + ROWS + row), p + row * D + col);
                 }
             }
         }
@@ -541,9 +607,13 @@ kv8_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
 #pragma unroll
             for (int e = 0; e < CPT / 2; ++e)
                 p[e] = (uint32_t)to16<T>(acc[2 * e] * inv) | ((uint32_t)to16<T>(acc[2 * e + 1] * inv) << 16);
+            if constexpr (CPT == 4) {
+                *reinterpret_cast<uint2*>(y) = make_uint2(p[0], p[1]);
+            } else {
 #pragma unroll
-            for (int e = 0; e < CPT / 8; ++e)
-                reinterpret_cast<uint4*>(y)[e] = make_uint4(p[4 * e], p[4 * e + 1], p[4 * e + 2], p[4 * e + 3]);
+                for (int e = 0; e < CPT / 8; ++e)
+                    reinterpret_cast<uint4*>(y)[e] = make_uint4(p[4 * e], p[4 * e + 1], p[4 * e + 2], p[4 * e + 3]);
+            }
         }
         // the next piece writes the shared O and the flag again
         asm volatile("bar.sync 1, 128;" ::: "memory");
@@ -568,26 +638,39 @@ constexpr int kMaxGrid = 1024;
 constexpr size_t kCntBytes = kMaxGrid * sizeof(int);
 static_assert(kCntBytes % 256 == 0, "the parts start 256-byte aligned");
 
-int attention_grid() {
-    const int g = kCtasPerSm * num_sms();
+int attention_grid(int nr) {
+    const int g = ctas_per_sm(nr) * num_sms();
     return g < kMaxGrid ? g : kMaxGrid;
+}
+
+template <typename T, int D, int NR>
+sq_status_t launch_rows(const char* name, const CUtensorMap& mk, const CUtensorMap& mv, const AttnArgs& a,
+                        cudaStream_t stream) {
+    using C = ACfg<D, NR>;
+    auto fn = kv8_attention_kernel<T, D, NR>;
+    if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM_ALLOC) != cudaSuccess)
+        return check_launch(name);
+    launch_pdl(fn, dim3(attention_grid(NR)), dim3(kThreadsA), C::SMEM_ALLOC, stream, mk, mv, a);
+    return check_launch(name);
 }
 
 template <typename T, int D>
 sq_status_t launch_attention(const char* name, const CUtensorMap& mk, const CUtensorMap& mv, const AttnArgs& a,
-                             cudaStream_t stream) {
-    auto fn = kv8_attention_kernel<T, D>;
-    if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)ACfg<D>::SMEM_ALLOC) != cudaSuccess)
-        return check_launch(name);
-    launch_pdl(fn, dim3(attention_grid()), dim3(kThreadsA), ACfg<D>::SMEM_ALLOC, stream, mk, mv, a);
-    return check_launch(name);
+                             int64_t max_q, cudaStream_t stream) {
+    if (max_q * a.G <= 8) return launch_rows<T, D, 1>(name, mk, mv, a, stream);
+    return launch_rows<T, D, 2>(name, mk, mv, a, stream);
 }
 
 }  // namespace
 
 size_t kv8_attention_workspace_bytes(int64_t T, int64_t Hq, int64_t D) {
     if (T <= 0 || Hq <= 0 || D <= 0) return kStatusBytes;
-    return kStatusBytes + kCntBytes + (size_t)attention_grid() * 2 * kRows * (size_t)(D + 2) * sizeof(float);
+    size_t part = 0;
+    for (int nr = 1; nr <= 2; ++nr) {
+        const size_t n = (size_t)attention_grid(nr) * 2 * (8 * nr) * (size_t)(D + 2) * sizeof(float);
+        part = n > part ? n : part;
+    }
+    return kStatusBytes + kCntBytes + part;
 }
 
 }  // namespace sq
@@ -647,8 +730,8 @@ extern "C" sq_status_t sq_kv8_attention(const void* Q, sq_dtype_t dt, int64_t T,
         return sq::set_error(SQ_ERR_CUDA, "%s: cuTensorMapEncodeTiled failed", name);
     cudaStream_t s = sq::as_cuda(stream);
     if (dt == SQ_BF16)
-        return D == 128 ? sq::launch_attention<__nv_bfloat16, 128>(name, mk, mv, a, s)
-                        : sq::launch_attention<__nv_bfloat16, 64>(name, mk, mv, a, s);
-    return D == 128 ? sq::launch_attention<__half, 128>(name, mk, mv, a, s)
-                    : sq::launch_attention<__half, 64>(name, mk, mv, a, s);
+        return D == 128 ? sq::launch_attention<__nv_bfloat16, 128>(name, mk, mv, a, max_q, s)
+                        : sq::launch_attention<__nv_bfloat16, 64>(name, mk, mv, a, max_q, s);
+    return D == 128 ? sq::launch_attention<__half, 128>(name, mk, mv, a, max_q, s)
+                    : sq::launch_attention<__half, 64>(name, mk, mv, a, max_q, s);
 }
