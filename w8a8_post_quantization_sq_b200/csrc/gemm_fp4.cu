@@ -12,13 +12,15 @@
 //     them the stage's block scales: the scale tiles are in global memory as
 //     tensor memory wants them, so a stage's scales of 128 rows are 2 KB (1 KB)
 //     in one piece;
-//   - the issuer copies each stage's scales to tensor memory (tcgen05.cp, which
-//     runs in issue order with the MMAs around it) and issues the MMAs;
+//   - four scale warps bring each stage's scales from shared to tensor memory
+//     (tcgen05.st, each its lane quarter) into one of two sets of columns, while
+//     the MMAs of the stage before run. (tcgen05.cp copies them without warps,
+//     but runs in one queue with the MMAs, about 50 cycles for each of a pair
+//     stage's 12: 4096 x 12288 x 12288 took 408 us so, in any order of issue.)
 //   - CTA pairs (256 x 256 tiles): two accumulators of 256 columns and the
-//     scales' 48 (24) columns exceed the 512 of tensor memory, so the second
-//     accumulator starts 48 columns early: the epilogue reads the shared
-//     columns first and hands them back, and the next tile's MMAs start while
-//     the rest is read;
+//     scales' two sets of 48 (24) columns exceed the 512 of tensor memory, so the
+//     accumulators share 96 (48): the epilogue reads the shared columns first
+//     and hands them back, and the next tile's MMAs start while the rest is read;
 //   - few tiles (decode batches): the k-loop of each 128 x 128 tile is cut into
 //     equal parts, one CTA each; partial sums are parked in the workspace and
 //     added in part order by the CTA that arrives last.
@@ -38,7 +40,8 @@ constexpr int BM = 128;
 constexpr int BK = 256;        // codes per stage: 128 bytes, one swizzle row
 constexpr int UMMA_K = 64;     // codes per MMA: 32 bytes
 constexpr int kEpiWarps = 8;   // two per TMEM lane quarter, each on half the tile's columns
-constexpr int kThreads = 64 + 32 * kEpiWarps;
+constexpr int kScaleWarps = 4;  // one per TMEM lane quarter
+constexpr int kThreads = 64 + 32 * (kEpiWarps + kScaleWarps);
 constexpr int kStgRow = 80;    // staging: 32 rows x 64 B + 16 B pad (the TMA-store box uses the first 2 KB)
 constexpr int kStgWarpBytes = 32 * kStgRow;
 static_assert(kStgWarpBytes % 512 == 0, "staging slots must keep the 64-byte swizzle's 512-byte alignment");
@@ -53,27 +56,29 @@ struct Cfg {
     static constexpr uint32_t B_BYTES = (BN / CG) * BK / 2;
     static constexpr uint32_t SA_BYTES = CHUNKS * kFp4TileBytes;
     static constexpr uint32_t SB_BYTES = NG * CHUNKS * kFp4TileBytes;
-    static constexpr uint32_t TX = A_BYTES + B_BYTES + SA_BYTES + SB_BYTES;
     static constexpr uint32_t A_OFF = 0;
     static constexpr uint32_t B_OFF = A_OFF + STAGES * A_BYTES;
     static constexpr uint32_t SA_OFF = B_OFF + STAGES * B_BYTES;
     static constexpr uint32_t SB_OFF = SA_OFF + STAGES * SA_BYTES;
-    static constexpr uint32_t BAR_OFF = SB_OFF + STAGES * SB_BYTES;  // full[S], empty[S], tfull[2], tempty[2], drain
-    static constexpr uint32_t MISC_OFF = BAR_OFF + (2 * STAGES + 5) * 8;
+    static constexpr uint32_t BAR_OFF = SB_OFF + STAGES * SB_BYTES;  // full[S], empty[S], tfull[2], tempty[2], drain, sfull[S], sready[S]
+    static constexpr uint32_t MISC_OFF = BAR_OFF + (4 * STAGES + 5) * 8;
     static constexpr uint32_t RW_OFF = (MISC_OFF + 16 + 15) / 16 * 16;
     static constexpr uint32_t RW_BYTES = kEpiWarps * 2 * (BN / 2) * 4;
     static constexpr uint32_t STG_OFF = (RW_OFF + RW_BYTES + 1023) / 1024 * 1024;
     static constexpr uint32_t SMEM = STG_OFF + kEpiWarps * kStgWarpBytes;
     static constexpr uint32_t SMEM_ALLOC = SMEM + 1024;
     static_assert(SMEM_ALLOC <= 232448, "over the 227 KB of shared memory a block may use");
-    // tensor memory: the scales in the last columns, the accumulators before them
+    // tensor memory: two sets of scales (the weight's, then X's) in the last
+    // columns, the accumulators before them
     static constexpr uint32_t TMEM_COLS = 512;
     static constexpr uint32_t SB_COLS = CHUNKS * NG * 4;
-    static constexpr uint32_t SFB_COL = TMEM_COLS - SB_COLS;
-    static constexpr uint32_t SFA_COL = SFB_COL - CHUNKS * 4;
-    static constexpr bool OVERLAP = 2 * BN > (int)SFA_COL;
-    static constexpr uint32_t ACC1 = OVERLAP ? SFA_COL - BN : BN;  // first column of the second accumulator
-    static_assert(!OVERLAP || (BN == 256 && BN - ACC1 <= 64), "the shared columns are two 32-column chunks at most");
+    static constexpr uint32_t SET_COLS = SB_COLS + CHUNKS * 4;
+    static constexpr uint32_t SF_COL = TMEM_COLS - 2 * SET_COLS;
+    static constexpr bool OVERLAP = 2 * BN > (int)SF_COL;
+    static constexpr uint32_t ACC1 = OVERLAP ? SF_COL - BN : BN;  // first column of the second accumulator
+    // 32-column chunks of a half accumulator that the next tile waits for
+    static constexpr int SHARED = OVERLAP ? (int)(BN - ACC1 + 31) / 32 : BN / 64;
+    static_assert(SHARED <= BN / 64, "the shared columns lie in one half of the accumulator");
     // Instruction descriptor: E2M1 operands (format 1 at bits 7 and 10), K-major,
     // N >> 3 at bit 17, scale format at bit 23 (0 E4M3, 1 E8M0), M >> 4 at bit
     // 24; which byte of a scale word to start from: bit 4 (B), bit 29 (A).
@@ -137,16 +142,21 @@ __device__ __forceinline__ void umma_fp4(uint32_t d, uint64_t a, uint64_t b, uin
             "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(sfa), "r"(sfb));
 }
 
-// One scale tile (512 bytes: 32 rows of 16) to four columns of tensor memory,
-// repeated in the four lane quarters; of a pair, each CTA from its own memory.
-template <int CG>
-__device__ __forceinline__ void copy_scales(uint32_t tmem, uint32_t saddr) {
-    // descriptor without swizzle: groups of 8 rows x 16 bytes, 128 bytes apart
-    const uint64_t d = (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(128 >> 4) << 32) | ((uint64_t)1 << 46);
-    if constexpr (CG == 1)
-        asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(d));
+// N words per lane (one of 32 lanes) to N columns of tensor memory.
+template <int N>
+__device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t* r) {
+    static_assert(N == 8 || N == 16, "columns per store");
+    if constexpr (N == 8)
+        asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]),
+                     "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                     : "memory");
     else
-        asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(d));
+        asm volatile(
+            "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
+                taddr),
+            "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+            "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+            : "memory");
 }
 
 template <int OUT>
@@ -261,6 +271,8 @@ gemm_fp4_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constan
     auto tfull_bar = [&](int a) { return bar0 + 8u * (2 * STAGES + a); };
     auto tempty_bar = [&](int a) { return bar0 + 8u * (2 * STAGES + 2 + a); };
     const uint32_t drain_bar = bar0 + 8u * (2 * STAGES + 4);
+    auto sfull_bar = [&](int s) { return bar0 + 8u * (2 * STAGES + 5 + s); };
+    auto sready_bar = [&](int s) { return bar0 + 8u * (3 * STAGES + 5 + s); };
     uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + C::MISC_OFF);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::MISC_OFF + 4);
 
@@ -270,6 +282,8 @@ gemm_fp4_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constan
         for (int s = 0; s < STAGES; ++s) {
             mbar_init(full_bar(s), 1);
             mbar_init(empty_bar(s), 1);
+            mbar_init(sfull_bar(s), 1);
+            mbar_init(sready_bar(s), kScaleWarps * CG);
         }
         for (int a = 0; a < 2; ++a) {
             mbar_init(tfull_bar(a), 1);
@@ -330,27 +344,32 @@ gemm_fp4_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constan
                         break;
                     }
                     const uint32_t fb = CG == 2 ? map_to_rank(full_bar(stage), 0) : full_bar(stage);
-                    if (rank == 0) mbar_expect_tx(full_bar(stage), CG * C::TX);
+                    if (rank == 0) mbar_expect_tx(full_bar(stage), CG * (C::A_BYTES + C::B_BYTES));
+                    mbar_expect_tx(sfull_bar(stage), C::SA_BYTES + C::SB_BYTES);
                     tma_load_3d<CG>(sbase + C::A_OFF + stage * C::A_BYTES, &tmap_a, fb, kb * (BK / 2), m0, 0);
                     tma_load_3d<CG>(sbase + C::B_OFF + stage * C::B_BYTES, &tmap_b, fb, kb * (BK / 2), n0, 0);
-                    tma_load_3d<CG>(sbase + C::SA_OFF + stage * C::SA_BYTES, &tmap_sa, fb, kb * (int)(C::SA_BYTES / 8),
-                                    m0 / 128, 0);
-                    tma_load_3d<CG>(sbase + C::SB_OFF + stage * C::SB_BYTES, &tmap_sb, fb, kb * (int)(C::SA_BYTES / 8), gn,
-                                    0);
+                    // the scales count on this CTA's own barrier: its scale warps wait for them
+                    tma_load_3d<1>(sbase + C::SA_OFF + stage * C::SA_BYTES, &tmap_sa, sfull_bar(stage),
+                                   kb * (int)(C::SA_BYTES / 8), m0 / 128, 0);
+                    tma_load_3d<1>(sbase + C::SB_OFF + stage * C::SB_BYTES, &tmap_sb, sfull_bar(stage),
+                                   kb * (int)(C::SA_BYTES / 8), gn, 0);
                     issued |= 1u << stage;
                     issued_phase = (issued_phase & ~(1u << stage)) | (phase << stage);
                     if (++stage == STAGES) stage = 0, phase ^= 1u;
                 }
             }
-            if (!ok && rank == 0)
+            if (!ok)
                 for (int s = 0; s < STAGES; ++s)
-                    if (issued >> s & 1u) wait_drain(full_bar(s), issued_phase >> s & 1u);
+                    if (issued >> s & 1u) {
+                        if (rank == 0) wait_drain(full_bar(s), issued_phase >> s & 1u);
+                        wait_drain(sfull_bar(s), issued_phase >> s & 1u);
+                    }
         }
     } else if (warp == 1) {
         if (lane == 0 && rank == 0) {
             // ---------------------------------------------------- MMA issuer
             int stage = 0, local = 0;
-            uint32_t phase = 0;
+            uint32_t phase = 0, set = 0;
             bool ok = true;
             for (int w = first; ok && w < items; w += step, ++local) {
                 const int part = w - w / p.splits * p.splits;
@@ -369,23 +388,16 @@ gemm_fp4_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constan
                 tc_fence_after();
                 const uint32_t d_tmem = tmem_base + (acc ? C::ACC1 : 0u);
                 for (int kb = k0; kb < k1; ++kb) {
-                    if (!wait_fast(full_bar(stage), phase, abort_flag, p.status, 0x8E3)) {
+                    if (!wait_fast(full_bar(stage), phase, abort_flag, p.status, 0x8E3) ||
+                        !wait_fast(sready_bar(stage), phase, abort_flag, p.status, 0x8E5)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
                     const uint32_t a_addr = sbase + C::A_OFF + stage * C::A_BYTES;
                     const uint32_t b_addr = sbase + C::B_OFF + stage * C::B_BYTES;
-                    const uint32_t sa_addr = sbase + C::SA_OFF + stage * C::SA_BYTES;
-                    const uint32_t sb_addr = sbase + C::SB_OFF + stage * C::SB_BYTES;
-#pragma unroll
-                    for (int c = 0; c < C::CHUNKS; ++c) {
-                        copy_scales<CG>(tmem_base + C::SFA_COL + c * 4, sa_addr + c * kFp4TileBytes);
-#pragma unroll
-                        for (int g = 0; g < C::NG; ++g)
-                            copy_scales<CG>(tmem_base + C::SFB_COL + (c * C::NG + g) * 4,
-                                            sb_addr + (g * C::CHUNKS + c) * kFp4TileBytes);
-                    }
+                    const uint32_t sfb = tmem_base + C::SF_COL + set * C::SET_COLS, sfa = sfb + C::SB_COLS;
+                    set ^= 1u;
                     // (codes past K are zero, but so may be all of an MMA's: skip those)
                     const int steps = min(BK / UMMA_K, (p.K - kb * BK + UMMA_K - 1) / UMMA_K);
 #pragma unroll
@@ -394,8 +406,7 @@ gemm_fp4_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constan
                         const int c = FMT == SQ_NVFP4 ? k : k >> 1;       // scale tile of this MMA
                         const int sf = FMT == SQ_NVFP4 ? 0 : (k & 1) * 2;  // first byte of its words
                         umma_fp4<FMT, CG>(d_tmem, sdesc(a_addr + k * (UMMA_K / 2)), sdesc(b_addr + k * (UMMA_K / 2)),
-                                          C::idesc(sf), tmem_base + C::SFA_COL + c * 4,
-                                          tmem_base + C::SFB_COL + c * C::NG * 4, (kb != k0 || k != 0) ? 1u : 0u);
+                                          C::idesc(sf), sfa + c * 4, sfb + c * C::NG * 4, (kb != k0 || k != 0) ? 1u : 0u);
                     }
                     umma_commit<CG>(empty_bar(stage));
                     if (++stage == STAGES) stage = 0, phase ^= 1u;
@@ -405,6 +416,50 @@ gemm_fp4_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constan
             }
             umma_commit<CG>(drain_bar, 1);
             wait_drain(drain_bar, 0);
+        }
+    } else if (warp >= 2 + kEpiWarps) {
+        // -------------------------------------------------- scale warps
+        // Each stage's scales, shared to tensor memory: a scale tile is four
+        // words per lane, the same in every lane quarter.
+        const uint32_t quarter = (uint32_t)((warp & 3) * 32) << 16;
+        int stage = 0, before = -2;  // `before`: the stage two stages ago, whose MMAs read this stage's set
+        uint32_t phase = 0, before_phase = 0, set = 0;
+        bool ok = true;
+        for (int w = first; ok && w < items; w += step) {
+            const int part = w - w / p.splits * p.splits;
+            const int k0 = (int)((int64_t)part * p.num_kb / p.splits);
+            const int k1 = (int)((int64_t)(part + 1) * p.num_kb / p.splits);
+            for (int kb = k0; kb < k1; ++kb) {
+                ok = wait_fast(sfull_bar(stage), phase, abort_flag, p.status, 0x8E6);
+                if (ok && before >= 0) ok = wait_fast(empty_bar(before), before_phase, abort_flag, p.status, 0x8E7);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                tc_fence_after();
+                uint32_t r[C::SET_COLS];
+                const uint4* sb = reinterpret_cast<const uint4*>(smem + C::SB_OFF + stage * C::SB_BYTES) + lane;
+                const uint4* sa = reinterpret_cast<const uint4*>(smem + C::SA_OFF + stage * C::SA_BYTES) + lane;
+#pragma unroll
+                for (int c = 0; c < C::CHUNKS; ++c) {
+#pragma unroll
+                    for (int g = 0; g < C::NG; ++g)
+                        *reinterpret_cast<uint4*>(r + (c * C::NG + g) * 4) = sb[(g * C::CHUNKS + c) * 32];
+                    *reinterpret_cast<uint4*>(r + C::SB_COLS + c * 4) = sa[c * 32];
+                }
+                const uint32_t to = tmem_base + quarter + C::SF_COL + set * C::SET_COLS;
+#pragma unroll
+                for (uint32_t i = 0; i + 16 <= C::SET_COLS; i += 16) tmem_st<16>(to + i, r + i);
+                if constexpr (C::SET_COLS % 16 == 8) tmem_st<8>(to + C::SET_COLS - 8, r + C::SET_COLS - 8);
+                asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    if constexpr (CG == 2) mbar_arrive_remote(map_to_rank(sready_bar(stage), 0));
+                    else mbar_arrive(sready_bar(stage));
+                }
+                set ^= 1u;
+                if (++before == STAGES) before = 0, before_phase ^= 1u;
+                if (++stage == STAGES) stage = 0, phase ^= 1u;
+            }
         }
     } else {
         // -------------------------------------------------------- epilogue
@@ -512,14 +567,14 @@ gemm_fp4_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constan
                 }
                 continue;
             }
-            // shared columns first: the upper half's last two chunks of the
-            // first accumulator, the lower half's first two of the second
-            const int turn = C::OVERLAP && acc == 0 && half == 1 ? NCH - 2 : 0;
+            // shared columns first: the upper half's last chunks of the first
+            // accumulator, the lower half's first ones of the second
+            const int turn = C::OVERLAP && acc == 0 && half == 1 ? NCH - C::SHARED : 0;
 #pragma unroll 1
             for (int i = 0; i < NCH; ++i) {
                 const int c = (i + turn) & (NCH - 1);
                 tmem_ld32(t_row + (uint32_t)(c * 32), r);
-                if (shares && i == (C::OVERLAP ? 1 : NCH - 1)) release_acc(acc);
+                if (shares && i == C::SHARED - 1) release_acc(acc);
                 if (row0 < p.M && c_base + c * 32 < p.N)
                     epi_chunk<OUT>(p, r, c * 32, c_base + c * 32, row0, rx, rw_w, bias_w, stg, lane, &tmap_y);
             }
