@@ -234,6 +234,10 @@ ATTN = [
     ([4, 4], [300, 77], 32, 2, 4, 64), ([1, 0, 3], [40, 9, 3], 16, 2, 2, 128), ([7], [7], 16, 1, 3, 128),
     ([40], [64], 16, 2, 1, 64), ([129, 1, 17], [129, 700, 300], 64, 2, 4, 128), ([1] * 33, [5 * i + 1 for i in range(33)], 16, 1, 8, 64),
     ([1, 1], [5000, 3], 16, 1, 2, 128), ([1], [3000], 128, 2, 32, 64), ([300], [1500], 16, 1, 2, 128),
+    # prompts (many rows per K/V head), among shorter sequences
+    ([700, 3, 257, 1], [1500, 300, 257, 90], 64, 2, 4, 128), ([64], [64], 16, 1, 1, 64), ([65], [193], 32, 2, 1, 64),
+    ([513, 128], [600, 128], 16, 1, 3, 128), ([1000], [1000], 128, 3, 1, 64), ([9, 2], [400, 2], 32, 1, 32, 128),
+    ([256, 0, 255, 1025], [257, 0, 2000, 1100], 16, 1, 2, 64),
 ]
 
 
@@ -246,7 +250,7 @@ def test_attention(new, lens, block, hkv, group, D, dt):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("new,lens,block,hkv,group,D", [ATTN[1], ATTN[6], ATTN[10]])
+@pytest.mark.parametrize("new,lens,block,hkv,group,D", [ATTN[1], ATTN[6], ATTN[10], ATTN[15], ATTN[21]])
 def test_attention_not_causal(new, lens, block, hkv, group, D):
     batch = ref.Batch(new, lens, hkv, D, block, seed=sum(lens))
     check_attention(batch, rows16(batch.T, hkv * group, D, BF, 1), causal=False)

@@ -155,7 +155,6 @@ __global__ void __launch_bounds__(kWarps * 32) kv8_append_kernel(const AppendArg
 
 }  // namespace
 
-// Sizes and pointers that appending to the cache and reading it share.
 sq_status_t check_kv8(const char* name, int64_t T, int64_t B, int64_t Hkv, int64_t D, int64_t block, int64_t num_blocks,
                       int64_t max_blocks, int64_t ldb) {
     SQ_REQUIRE(T >= 0 && B >= 0 && Hkv > 0 && num_blocks > 0 && max_blocks > 0 && ldb >= max_blocks,

@@ -40,9 +40,6 @@
 
 namespace sq {
 
-sq_status_t check_kv8(const char* name, int64_t T, int64_t B, int64_t Hkv, int64_t D, int64_t block, int64_t num_blocks,
-                      int64_t max_blocks, int64_t ldb);
-
 namespace {
 
 constexpr int kTile = 64;     // keys per stage
@@ -50,26 +47,10 @@ constexpr int kSub = 16;      // keys per warp of a stage
 constexpr int kCWarps = 4;    // consumer warps
 constexpr int kThreadsA = 32 * (kCWarps + 1);
 constexpr int kStages = 3;
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kSlack = 8.0f;
+// sequences of more rows than this go to the prompt kernel where one is launched
+constexpr int64_t kRowLimit = 64;
 // blocks per SM by row groups of 8: registers (accumulators) and shared memory
 constexpr int ctas_per_sm(int nr) { return nr == 1 ? 3 : 2; }
-
-struct AttnArgs {
-    const void* Q;
-    void* Y;
-    int64_t ldq, ldy, T, ldb, num_blocks;
-    const int32_t* cu;
-    const int32_t* lens;
-    const int32_t* table;
-    const float* kqs;
-    const float* vqs;
-    int B, Hkv, G, block, box, max_blocks, causal;
-    float scale;
-    int* status;
-    int* cnt;     // [grid] key tiles counted in per row tile (zero between launches)
-    float* part;  // [grid][2]: O [rows][D], m [rows], l [rows]
-};
 
 template <int D, int NR>
 struct ACfg {
@@ -86,11 +67,6 @@ struct ACfg {
     static constexpr uint32_t SMEM_ALLOC = SMEM + 1024;
 };
 
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
 __device__ __forceinline__ uint4 lds128(uint32_t a) {
     uint4 v;
     asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
@@ -108,19 +84,6 @@ __device__ __forceinline__ void mma16816(float* d, const uint32_t* a, uint32_t b
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-// Bytes of u (code + 128) as fp16 integers: 0x6400 + u is 1024 + u in fp16, so
-// subtracting 1152 leaves the code, exactly.
-__device__ __forceinline__ uint32_t half2_of(uint32_t u, uint32_t sel) {
-    const uint32_t h = __byte_perm(u, 0x64646464u, sel);
-    uint32_t r;
-    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(h), "r"(0x64806480u));
-    return r;
-}
-__device__ __forceinline__ uint32_t pack_half2(float a, float b) {
-    const __half2 h = __floats2half2_rn(a, b);
-    return *reinterpret_cast<const uint32_t*>(&h);
-}
-
 // An 8 x 8 tile of 16-bit elements transposed across the warp.
 __device__ __forceinline__ uint32_t movmatrix(uint32_t v) {
     uint32_t r;
@@ -128,27 +91,14 @@ __device__ __forceinline__ uint32_t movmatrix(uint32_t v) {
     return r;
 }
 
-// One sequence's share of the work.
-struct Seq {
-    int64_t lo;  // first new token
-    int n, len, rt, tiles;
-    __device__ int64_t work(int Hkv) const { return (int64_t)Hkv * rt * tiles; }
-};
-template <int ROWS>
-__device__ __forceinline__ Seq seq_of(const AttnArgs& a, int b) {
-    Seq s;
-    const int64_t lo = min(max((int64_t)__ldg(a.cu + b), (int64_t)0), a.T);
-    const int64_t hi = min((int64_t)__ldg(a.cu + b + 1), a.T);
-    s.lo = lo;
-    s.n = (int)max(hi - lo, (int64_t)0);
-    s.len = min(max(__ldg(a.lens + b), 0), a.max_blocks * a.block);
-    s.rt = (int)(((int64_t)s.n * a.G + ROWS - 1) / ROWS);
-    s.tiles = max((s.len + kTile - 1) / kTile, 1);  // a sequence without keys still has rows to write
-    return s;
-}
-
 // A block's range of the list of key tiles, as pieces: the part of the range
 // inside one row tile. Every warp walks the same sequence.
+template <int ROWS>
+__device__ __forceinline__ Seq seq_of(const AttnArgs& a, int b) {
+    Seq s = seq_of<ROWS, kTile>(a, b);
+    if ((int64_t)s.n * a.G > a.row_limit) s.rt = 0;
+    return s;
+}
 template <int ROWS>
 struct Walk {
     int64_t it, end, total, units;
@@ -211,11 +161,7 @@ struct Walk {
         k0 = 0;
         ++item;
     }
-    // Keys that the row tile's last row sees, and those that row `row` sees.
-    __device__ __forceinline__ int seen(const AttnArgs& a, int row) const {
-        const int i = min(row / a.G, s.n - 1);
-        return a.causal ? max(min(s.len - s.n + i + 1, s.len), 0) : s.len;
-    }
+    __device__ __forceinline__ int seen(const AttnArgs& a, int row) const { return seen_by(a, s, row); }
 };
 
 template <typename T, int D, int NR>
@@ -620,19 +566,6 @@ kv8_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
     }
 }
 
-// The cache as [num_blocks, Hkv * block, D] bytes, box D x box x 1.
-bool make_map_kv(CUtensorMap* m, const int8_t* base, int64_t num_blocks, int64_t rows, int64_t D, int box) {
-    auto fn = encode_fn();
-    if (!fn) return false;
-    cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)rows, (cuuint64_t)num_blocks};
-    cuuint64_t strides[2] = {(cuuint64_t)D, (cuuint64_t)(rows * D)};
-    cuuint32_t bx[3] = {(cuuint32_t)D, (cuuint32_t)box, 1};
-    cuuint32_t estr[3] = {1, 1, 1};
-    return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<int8_t*>(base), dims, strides, bx, estr,
-              CU_TENSOR_MAP_INTERLEAVE_NONE, D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
-              CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 // Counters at a fixed place for every size, one per block of the largest grid.
 constexpr int kMaxGrid = 1024;
 constexpr size_t kCntBytes = kMaxGrid * sizeof(int);
@@ -725,10 +658,18 @@ extern "C" sq_status_t sq_kv8_attention(const void* Q, sq_dtype_t dt, int64_t T,
     a.cnt = reinterpret_cast<int*>(static_cast<uint8_t*>(workspace) + sq::kStatusBytes);
     a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + sq::kStatusBytes + sq::kCntBytes);
     CUtensorMap mk, mv;
-    if (!sq::make_map_kv(&mk, Kc, num_blocks, Hkv * block, D, a.box) ||
-        !sq::make_map_kv(&mv, Vc, num_blocks, Hkv * block, D, a.box))
+    if (!sq::make_map_kv(&mk, Kc, num_blocks, Hkv * block, D, a.box, true) ||
+        !sq::make_map_kv(&mv, Vc, num_blocks, Hkv * block, D, a.box, true))
         return sq::set_error(SQ_ERR_CUDA, "%s: cuTensorMapEncodeTiled failed", name);
     cudaStream_t s = sq::as_cuda(stream);
+    // prompts and single tokens may share a batch: each kernel takes its
+    // sequences; without long ones (as the caller says) one kernel takes all
+    a.row_limit = INT64_MAX;
+    if (max_q > sq::kRowLimit / a.G) {
+        a.row_limit = sq::kRowLimit;
+        const sq_status_t ps = sq::launch_kv8_prefill(name, dt, D, Kc, Vc, a, s);
+        if (ps != SQ_OK) return ps;
+    }
     if (dt == SQ_BF16)
         return D == 128 ? sq::launch_attention<__nv_bfloat16, 128>(name, mk, mv, a, max_q, s)
                         : sq::launch_attention<__nv_bfloat16, 64>(name, mk, mv, a, max_q, s);
