@@ -269,6 +269,25 @@ def test_attention_rows_without_keys():
 
 
 @pytest.mark.gpu
+def test_prompt_rows_without_keys():
+    """The same for sequences of many rows."""
+    batch = ref.Batch([2, 1, 50, 200, 90], [10, 0, 30, 70, 0], 2, 128, 16, seed=1)
+    q = rows16(batch.T, 8, 128, BF, 1)
+    y = run_attention(batch, q, 0.09, True)
+    check_attention(batch, q, 0.09, y=y)
+    assert bool((y[2:23] == 0).all() and (y[53:183] == 0).all() and (y[253:343] == 0).all())
+    check_attention(batch, q, 0.09, causal=False)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("scale", [0.0, -0.05, 3.0])
+def test_attention_any_scale(scale):
+    """Scale zero (equal weights), negative, and large."""
+    batch = ref.Batch([1, 100], [90, 150], 2, 64, 16, seed=3)
+    check_attention(batch, rows16(101, 4, 64, FP, 2, 0.2), scale)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("spread", [1e-6, 1e5])
 def test_attention_scales_far_apart(spread):
     """Blocks whose V (and K) scales differ by many orders of magnitude; a block of zeros."""
@@ -284,14 +303,14 @@ def test_attention_scales_far_apart(spread):
 @pytest.mark.gpu
 def test_attention_peaked_and_shifted_scores():
     """Scores far from zero, growing along the sequence (the running maximum moves all the time) or falling."""
-    for sign in (1.0, -1.0):
-        batch = ref.Batch([1, 3], [600, 200], 1, 64, 16, seed=4)
+    for sign, new in ((1.0, [1, 3]), (-1.0, [1, 3]), (1.0, [150, 130]), (-1.0, [150, 130])):
+        batch = ref.Batch(new, [600, 200], 1, 64, 16, seed=4)
         for b in range(2):
             for j, blk in enumerate(batch.table[b]):
                 batch.k[blk, :, :, 0] = 100
                 batch.kqs[blk] = ref.f32(100.0 / (j + 1))
                 batch.k[blk, :, :, 1:] = np.clip(batch.k[blk, :, :, 1:] // 32, -1, 1)
-        q = rows16(4, 4, 64, BF, 5, 0.25)
+        q = rows16(batch.T, 4, 64, BF, 5, 0.25)
         q[:, :, 0] = sign * 4.0
         check_attention(batch, q, 0.5)
 
@@ -335,6 +354,34 @@ def test_attention_bad_values_stay_where_they_are_read():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("D", [64, 128])
+def test_prompt_bad_values_stay_where_they_are_read(D):
+    """The same for sequences of many rows: only the rows from the bad block on."""
+    bs = 16
+    batch = ref.Batch([80, 70, 1], [130, 70, 40], 1, D, bs, seed=7, width=12)
+    for b, used in enumerate((9, 5, 3)):
+        batch.kqs[batch.table[b, used:]] = batch.vqs[batch.table[b, used:]] = np.nan
+        batch.table[b, used + 1 :] = -1
+    q = rows16(151, 2, D, BF, 8)
+    dev = batch.gpu()
+    clean = run_attention(batch, q, 0.1, True, dev=dev)
+    check_attention(batch, q, 0.1, y=clean)
+    for name in ("kqs", "vqs"):
+        spoilt = batch.gpu()
+        spoilt[name][batch.table[0, 5]] = float("nan")  # positions 80 .. 95
+        spoilt["table"][1, 3] = batch.num  # positions 48 .. 63: outside the cache
+        q2 = q.clone()
+        q2[3, 1, 7] = float("inf")
+        y = run_attention(batch, q2, 0.1, True, dev=spoilt)
+        bad = torch.zeros((151, 2, D), dtype=torch.bool)
+        bad[30:80] = True  # tokens at positions 50 + i
+        bad[80 + 48 : 150] = True
+        bad[3, 1] = True
+        assert torch.equal(y.isnan().cpu(), bad)
+        assert torch.equal(y[~bad.cuda()], clean[~bad.cuda()])
+
+
+@pytest.mark.gpu
 def test_attention_rows_behind_the_last_sequence():
     batch = ref.Batch([2, 1], [30, 70], 1, 64, 16, seed=8)
     q = rows16(9, 2, 64, BF, 1)
@@ -347,7 +394,8 @@ def test_attention_rows_behind_the_last_sequence():
 def test_attention_same_bits_every_time():
     """One workspace for batches of different lengths in turn; equal bits; the counters are zero again."""
     ws = sq.workspace(sq.SQ_OP_KV8_ATTENTION, 64, 16, 128)
-    for new, lens in (([1], [4000]), ([1] * 5, [900, 1, 64, 333, 2000]), ([9, 1], [100, 1500]), ([1], [4000])):
+    for new, lens in (([1], [4000]), ([1] * 5, [900, 1, 64, 333, 2000]), ([9, 1], [100, 1500]),
+                      ([300, 1, 400], [900, 1500, 400]), ([1], [4000])):
         batch = ref.Batch(new, lens, 2, 128, 16, seed=9)
         dev = batch.gpu()
         q = rows16(batch.T, 8, 128, BF, 1)

@@ -6,7 +6,7 @@
 // softmax's exponent, P in fp16 below 2^8, a running maximum that moves only
 // when a score passes it by 2^8. Here both products run on tcgen05 (kind::f16):
 //   S = Q K^T   128 rows x 128 keys, both from shared memory
-//   O += P V    P from tensor memory (it overwrites S's columns), V from shared
+//   O += P V    P from tensor memory (it overwrites half of S), V from shared
 //               memory with the columns contiguous (MN-major), as it lies in
 //               the cache
 // A CTA (one per SM, persistent) takes 256 rows of one sequence and K/V head as
@@ -17,13 +17,13 @@
 //                      rescales O and writes Y
 //   warps 8..11        int8 K and V tiles to fp16 tiles (128-byte swizzle): 128
 //                      x D codes are converted once for 256 rows
-//   warp 12            TMA of the int8 tiles, warp 13 the MMAs
-// Items are (sequence, 256 rows, head), the rows with the most keys first.
+//   warp 12            TMA of the int8 tiles, warp 13 the MMAs (14, 15 idle)
+// Items are (sequence, 256 rows, head), the last rows of every sequence first (they
+// see the most keys), dealt to the CTAs forth and back.
 // What bounds it: 128 x 128 scores take 512 cycles of the tensor core for each
 // product at D = 128 and 1024 of the exponential unit, two tiles 2048 of either.
 // Every wait is bounded (about 2 s), code 0x9E1 + role in the status word.
 #include <climits>
-#include <cstring>
 
 #include "sq_internal.h"
 #include "sq_kv8.cuh"
@@ -36,7 +36,11 @@ constexpr int kKeys = 128;
 constexpr int kTileRows = 128;
 constexpr int kItemRows = 2 * kTileRows;
 constexpr int kRaw = 3, kF16 = 3;  // ring stages: int8 tiles, fp16 tiles
-constexpr int kThreadsP = 14 * 32;
+constexpr int kThreadsP = 16 * 32;
+// Registers per thread: 128 at launch, dealt out again by warpgroup (two softmax
+// groups, conversion, TMA and MMA).
+constexpr int kRegsSoftmax = 160, kRegsConvert = 96, kRegsIssue = 96;
+static_assert(2 * kRegsSoftmax + kRegsConvert + kRegsIssue <= 4 * 128, "more registers than the block was launched with");
 
 template <int D>
 struct PCfg {
@@ -85,54 +89,73 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
         "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
         : "memory");
 }
+// 16 columns, with the wait in the same statement.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t* r) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
+}
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// The CTA's items in turn: item index -> sequence, head, rows, key tiles. Every
-// warp walks them together (32 sequences a look).
+// The CTA's items in turn. Level k of the order holds the k-th row block from
+// the end of every sequence that has one, for every head. Every warp walks the
+// items together (32 sequences a look).
 struct Items {
-    int64_t next_item, before, total_in;  // items before the sequences of `base`, and in them
-    int base;
+    int64_t before, count;  // items of the levels before `level`, and of it
+    int level, round;
     Seq s;
     int b, h, r0;
     int tiles[2];  // key tiles of each row tile
     int vis;       // keys that the item's last row sees
-    int64_t inc, mine;
 
+    // row blocks of sequence i
+    __device__ __forceinline__ int blocks_of(const AttnArgs& a, int i) const {
+        if (i >= a.B) return 0;
+        const Seq t = seq_of<kItemRows, kKeys>(a, i);
+        return (int64_t)t.n * a.G > a.row_limit ? t.rt : 0;
+    }
     __device__ __forceinline__ void look(const AttnArgs& a, int lane) {
-        mine = 0;
-        if (base + lane < a.B) {
-            const Seq t = seq_of<kItemRows, kKeys>(a, base + lane);
-            if ((int64_t)t.n * a.G > a.row_limit) mine = (int64_t)t.rt * a.Hkv;
-        }
-        inc = mine;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int64_t up = __shfl_up_sync(0xffffffffu, inc, o);
-            if (lane >= o) inc += up;
-        }
-        total_in = __shfl_sync(0xffffffffu, inc, 31);
+        int n = 0;
+        for (int base = 0; base < a.B; base += 32)
+            n += __popc(__ballot_sync(0xffffffffu, blocks_of(a, base + lane) > level));
+        count = (int64_t)n * a.Hkv;
     }
     __device__ __forceinline__ void init(const AttnArgs& a, int lane) {
-        next_item = blockIdx.x;
         before = 0;
-        base = 0;
+        level = round = 0;
         look(a, lane);
     }
     __device__ __forceinline__ bool next(const AttnArgs& a, int lane) {
-        while (next_item >= before + total_in) {
-            before += total_in;
-            base += 32;
-            if (base >= a.B) return false;
+        const int64_t at = (int64_t)round * gridDim.x + ((round & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+        ++round;
+        while (at >= before + count) {
+            if (count == 0) return false;
+            before += count;
+            ++level;
             look(a, lane);
         }
-        const int l = __ffs(__ballot_sync(0xffffffffu, before + inc > next_item)) - 1;
-        b = base + l;
-        const int64_t first = before + __shfl_sync(0xffffffffu, inc - mine, l);
+        const int idx = (int)(at - before);
+        int nth = idx / a.Hkv;  // the nth sequence with a block of this level
+        h = idx - nth * a.Hkv;
+        for (int base = 0;; base += 32) {
+            const int blocks = blocks_of(a, base + lane);
+            const unsigned has = __ballot_sync(0xffffffffu, blocks > level);
+            const int n = __popc(has);
+            if (nth < n) {
+                unsigned left = has;
+                while (nth-- > 0) left &= left - 1;
+                const int l = __ffs(left) - 1;
+                b = base + l;
+                r0 = (__shfl_sync(0xffffffffu, blocks, l) - 1 - level) * kItemRows;
+                break;
+            }
+            nth -= n;
+        }
         s = seq_of<kItemRows, kKeys>(a, b);
-        const int idx = (int)(next_item - first);
-        const int back = idx / a.Hkv;
-        h = idx - back * a.Hkv;
-        r0 = (s.rt - 1 - back) * kItemRows;
         const int rows = s.n * a.G;
         vis = seen_by(a, s, min(r0 + kItemRows, rows) - 1);
 #pragma unroll
@@ -140,7 +163,6 @@ struct Items {
             const int f = r0 + x * kTileRows;
             tiles[x] = f < rows ? (seen_by(a, s, min(f + kTileRows, rows) - 1) + kKeys - 1) / kKeys : 0;
         }
-        next_item += gridDim.x;
         return true;
     }
 };
@@ -198,11 +220,15 @@ kv8_prefill_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_const
     const uint32_t tmem = *tmem_holder;
     pdl_wait();
     pdl_trigger();
+    auto wait = [&](uint32_t bar, uint32_t parity, int code) {
+        return wait_bounded_inline(bar, parity, abort_flag, a.status, code, kTimeoutNs);
+    };
     Items it;
     it.init(a, lane);
     bool ok = true;
     if (warp < 8) {
         // ------------------------------------------------------ softmax
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
         const int x = warp >> 2;
         const int row = (warp & 3) * 32 + lane;  // row of the tile, and lane of tensor memory
         const uint32_t quarter = (uint32_t)((warp & 3) * 32) << 16;
@@ -232,7 +258,8 @@ kv8_prefill_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_const
                 unpack<T>(make_uint4(max(m2 & 0xffffu, m2 >> 16), 0, 0, 0), top);
                 const uint32_t field = min(max(__float_as_uint(top[0]) >> 23, 1u), 253u);
                 const float down = copysignf(__uint_as_float((254u - field) << 23), a.scale);
-                crow = fabsf(a.scale) * kLog2e * __uint_as_float(field << 23);
+                // (never 0: a masked score is -inf before it is multiplied)
+                crow = fmaxf(fabsf(a.scale) * kLog2e * __uint_as_float(field << 23), 1.17549435e-38f);
                 uint8_t* base = smem + C::Q_OFF + x * C::TILE + row * 128;
 #pragma unroll
                 for (int e = 0; e < D / 8; ++e) {
@@ -269,80 +296,111 @@ kv8_prefill_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_const
             for (int j = 0; j < tiles; ++j) {
                 const float my_k = __frcp_rn(next.x), my_v = next.y, my_lv = -__log2f(next.y);
                 if (j + 1 < tiles) next = scales_of(j + 1);
-                ok = wait_fast(s_full(x), s_phase, abort_flag, a.status, 0x9E1);
+                ok = wait(s_full(x), s_phase, 0x9E1);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 s_phase ^= 1u;
                 tc_fence_after();
                 const int key0 = j * kKeys;
                 const bool masked = __any_sync(0xffffffffu, key0 + kKeys > vis);
-                float tm = -INFINITY;
-                uint32_t s[32];
+                // per 16 keys: score factor and -log2 of the V scale; of keys that
+                // this row does not see nothing is taken, whatever their scales
+                float f[8], lv[8];
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    tmem_ld32(t_s + c * 32, s);
-#pragma unroll
-                    for (int hb = 0; hb < 2; ++hb) {
-                        const float f = crow * __shfl_sync(0xffffffffu, my_k, 2 * c + hb);
-                        const float lv = __shfl_sync(0xffffffffu, my_lv, 2 * c + hb);
-                        float q = -INFINITY;
-                        if (!masked) {
-#pragma unroll
-                            for (int e = 0; e < 16; ++e) q = fmaxf(q, __uint_as_float(s[16 * hb + e]));
-                            tm = fmaxf(tm, fmaf(q, f, lv));
-                        } else {
-#pragma unroll
-                            for (int e = 0; e < 16; ++e)
-                                if (key0 + 32 * c + 16 * hb + e < vis)
-                                    q = fmaxf(q, fmaf(__uint_as_float(s[16 * hb + e]), f, lv));
-                            tm = fmaxf(tm, q);
-                        }
-                    }
+                for (int q = 0; q < 8; ++q) {
+                    f[q] = crow * __shfl_sync(0xffffffffu, my_k, q);
+                    lv[q] = __shfl_sync(0xffffffffu, my_lv, q);
+                    if (key0 + 16 * q >= vis) f[q] = 1.0f, lv[q] = 0.0f;
                 }
-                if (__any_sync(0xffffffffu, tm > m + kSlack)) {
-                    const float to = tm > m + kSlack ? tm : m;
-                    const float f = to == -INFINITY ? 1.0f : ex2(m - to);
+                float tm = -INFINITY;
+                auto mask = [&](uint32_t* s, int c) {
+                    if (masked)
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            if (key0 + 32 * c + e >= vis) s[e] = 0xff800000u;
+                };
+                auto top = [&](const uint32_t* s, int c) {
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        float v = __uint_as_float(s[16 * q]);
+#pragma unroll
+                        for (int e = 1; e < 16; ++e) v = fmaxf(v, __uint_as_float(s[16 * q + e]));
+                        tm = fmaxf(tm, fmaf(v, f[2 * c + q], lv[2 * c + q]));
+                    }
+                };
+                // the maximum: chunks 0 and 1, then 2 and 3, which stay
+                uint32_t sa[32], sb[32];
+                tmem_ld32_async(t_s, sa);
+                tmem_ld32_async(t_s + 32, sb);
+                tmem_wait(sa);
+                tmem_wait(sb);
+                mask(sa, 0);
+                mask(sb, 1);
+                top(sa, 0);
+                top(sb, 1);
+                tmem_ld32_async(t_s + 64, sa);
+                tmem_ld32_async(t_s + 96, sb);
+                tmem_wait(sa);
+                tmem_wait(sb);
+                mask(sa, 2);
+                mask(sb, 3);
+                top(sa, 2);
+                top(sb, 3);
+                const bool move = tm > m + kSlack;
+                if (__any_sync(0xffffffffu, move)) {
+                    const float to = move ? tm : m;
+                    const float r = to == -INFINITY ? 1.0f : ex2(m - to);
                     m = to;
-                    l *= f;
+                    l *= r;
                     if (j > 0) {
                         // (the scores' barrier says that the product before them is complete)
 #pragma unroll 1
-                        for (int c = 0; c < D / 32; ++c) {
-                            tmem_ld32(t_o + c * 32, s);
+                        for (int c = 0; c < D / 16; ++c) {
+                            uint32_t o[16];
+                            tmem_ld16(t_o + c * 16, o);
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) s[e] = __float_as_uint(__uint_as_float(s[e]) * f);
-                            tmem_st16(t_o + c * 32, s);
-                            tmem_st16(t_o + c * 32 + 16, s + 16);
+                            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * r);
+                            tmem_st16(t_o + c * 16, o);
                         }
                     }
                 }
                 const float mu = m == -INFINITY ? 0.0f : m;
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    tmem_ld32(t_s + c * 32, s);
+                // P of chunk c goes to the first half of the chunk's own columns
+                auto weights = [&](const uint32_t* s, int c) {
                     uint32_t p[16];
 #pragma unroll
-                    for (int hb = 0; hb < 2; ++hb) {
-                        const float f = crow * __shfl_sync(0xffffffffu, my_k, 2 * c + hb);
-                        const float lv = __shfl_sync(0xffffffffu, my_lv, 2 * c + hb) - mu;
-                        const float vq = __shfl_sync(0xffffffffu, my_v, 2 * c + hb);
-                        float sum = 0.0f;
+                    for (int q = 0; q < 2; ++q) {
+                        const int k = 2 * c + q;
+                        const uint64_t f2 = pk2(f[k], f[k]), c2 = pk2(lv[k] - mu, lv[k] - mu);
+                        uint64_t sum2 = 0;
 #pragma unroll
-                        for (int e = 0; e < 16; e += 2) {
-                            float p0 = ex2(fmaf(__uint_as_float(s[16 * hb + e]), f, lv));
-                            float p1 = ex2(fmaf(__uint_as_float(s[16 * hb + e + 1]), f, lv));
-                            if (masked) {
-                                if (key0 + 32 * c + 16 * hb + e >= vis) p0 = 0.0f;
-                                if (key0 + 32 * c + 16 * hb + e + 1 >= vis) p1 = 0.0f;
-                            }
-                            sum += p0 + p1;
-                            p[8 * hb + e / 2] = pack_half2(p0, p1);
+                        for (int e = 0; e < 8; ++e) {
+                            float p0, p1;
+                            upk2(fma2(pk2(__uint_as_float(s[16 * q + 2 * e]), __uint_as_float(s[16 * q + 2 * e + 1])), f2,
+                                      c2),
+                                 p0, p1);
+                            p0 = ex2(p0);
+                            p1 = ex2(p1);
+                            sum2 = e == 0 ? pk2(p0, p1) : add2(sum2, pk2(p0, p1));
+                            p[8 * q + e] = pack_half2(p0, p1);
                         }
-                        // (a row that sees none of these keys takes nothing from their scale)
-                        if (!masked || key0 + 32 * c + 16 * hb < vis) l = fmaf(sum, vq, l);
+                        float a0, a1;
+                        upk2(sum2, a0, a1);
+                        const float vq = __shfl_sync(0xffffffffu, my_v, k);
+                        l = fmaf(a0 + a1, key0 + 16 * k < vis ? vq : 0.0f, l);
                     }
-                    tmem_st16(t_s + c * 16, p);
-                }
+                    tmem_st16(t_s + c * 32, p);
+                };
+                weights(sa, 2);
+                tmem_ld32_async(t_s, sa);
+                weights(sb, 3);
+                tmem_ld32_async(t_s + 32, sb);
+                tmem_wait(sa);
+                tmem_wait(sb);
+                mask(sa, 0);
+                mask(sb, 1);
+                weights(sa, 0);
+                weights(sb, 1);
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
@@ -352,7 +410,7 @@ kv8_prefill_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_const
             const float inv = (m == -INFINITY && l == 0.0f) ? 0.0f : __frcp_rn(l);
             T* y = static_cast<T*>(a.Y) + at * a.ldy + head;
             if (tiles > 0) {
-                ok = wait_fast(o_full(x), o_phase, abort_flag, a.status, 0x9E2);
+                ok = wait(o_full(x), o_phase, 0x9E2);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 o_phase ^= 1u;
@@ -382,14 +440,15 @@ kv8_prefill_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_const
         }
     } else if (warp < 12) {
         // ------------------------------------------------------ conversion
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsConvert));
         const int t = threadIdx.x - 256;
         int rs = 0, fs = 0;
         uint32_t rp = 0, fp = 0;
         while (ok && it.next(a, lane)) {
             const int n = 2 * max(it.tiles[0], it.tiles[1]);
             for (int j = 0; ok && j < n; ++j) {
-                ok = wait_fast(raw_full(rs), rp, abort_flag, a.status, 0x9E3) &&
-                     wait_fast(f_empty(fs), fp ^ 1u, abort_flag, a.status, 0x9E4);
+                ok = wait(raw_full(rs), rp, 0x9E3) &&
+                     wait(f_empty(fs), fp ^ 1u, 0x9E4);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 const uint8_t* src = smem + C::R_OFF + rs * C::RAW;
@@ -429,6 +488,7 @@ kv8_prefill_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_const
         }
     } else if (warp == 12) {
         // ------------------------------------------------------ TMA
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
         int rs = 0;
         uint32_t rp = 0, issued = 0, issued_phase = 0;
         const int box = a.box, per_box = box / 16;
@@ -452,7 +512,7 @@ kv8_prefill_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_const
                     const int boxes = __popc(__ballot_sync(0xffffffffu, copy));
 #pragma unroll
                     for (int v = 0; v < 2; ++v) {
-                        ok = wait_fast(raw_empty(rs), rp ^ 1u, abort_flag, a.status, 0x9E5);
+                        ok = wait(raw_empty(rs), rp ^ 1u, 0x9E5);
                         ok = __all_sync(0xffffffffu, ok);
                         if (!ok) break;
                         if (lane == 0) mbar_expect_tx(raw_full(rs), (uint32_t)(boxes * box * D));
@@ -469,9 +529,10 @@ kv8_prefill_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_const
         }
         if (!ok)
             for (int s = 0; s < kRaw; ++s)
-                if (issued >> s & 1u) wait_drain(raw_full(s), issued_phase >> s & 1u);
-    } else {
+                if (issued >> s & 1u) wait_drain_inline(raw_full(s), issued_phase >> s & 1u);
+    } else if (warp == 13) {
         // ------------------------------------------------------ MMA
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
         int fs = 0;  // stage of the next fp16 tile in the order K0 V0 K1 V1 ...
         uint32_t fp = 0, q_phase = 0, p_phase[2] = {0, 0};
         while (ok && it.next(a, lane)) {
@@ -479,7 +540,7 @@ kv8_prefill_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_const
                 const int n0 = it.tiles[0], n1 = it.tiles[1], n = max(n0, n1);
                 auto take = [&](int& stage) {  // waits for the next fp16 tile
                     stage = fs;
-                    const bool got = wait_fast(f_full(fs), fp, abort_flag, a.status, 0x9E6);
+                    const bool got = wait(f_full(fs), fp, 0x9E6);
                     if (++fs == kF16) fs = 0, fp ^= 1u;
                     tc_fence_after();
                     return got;
@@ -493,8 +554,8 @@ kv8_prefill_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_const
                     }
                     umma_commit<1>(s_full(x));
                 };
-                ok = wait_fast(q_ready(0), q_phase, abort_flag, a.status, 0x9E7) &&
-                     wait_fast(q_ready(1), q_phase, abort_flag, a.status, 0x9E7);
+                ok = wait(q_ready(0), q_phase, 0x9E7) &&
+                     wait(q_ready(1), q_phase, 0x9E7);
                 tc_fence_after();
                 int ks = 0, vs = 0;
                 if (ok && n > 0) {
@@ -512,14 +573,14 @@ kv8_prefill_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_const
                     for (int x = 0; ok && x < 2; ++x) {
                         const int nx = x ? n1 : n0;
                         if (j < nx) {
-                            ok = wait_fast(p_full(x), p_phase[x], abort_flag, a.status, 0x9E8);
+                            ok = wait(p_full(x), p_phase[x], 0x9E8);
                             if (!ok) break;
                             p_phase[x] ^= 1u;
                             tc_fence_after();
                             const uint32_t vb = sbase + C::F_OFF + vs * C::TILE;
 #pragma unroll
                             for (int k = 0; k < kKeys / 16; ++k)
-                                umma_ts(tmem + C::O_COL + x * D, tmem + x * 128 + k * 8,
+                                umma_ts(tmem + C::O_COL + x * D, tmem + x * 128 + (k >> 1) * 32 + (k & 1) * 8,
                                         sdesc_mn(vb + k * 16 * 128, C::HALF), C::IDESC_O, (j != 0 || k != 0) ? 1u : 0u);
                             if (j + 1 == nx) umma_commit<1>(o_full(x));
                         }
@@ -539,8 +600,10 @@ kv8_prefill_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_const
         }
         if (lane == 0) {
             umma_commit<1>(drain_bar);
-            wait_drain(drain_bar, 0);
+            wait_drain_inline(drain_bar, 0);
         }
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
     }
     __syncwarp();
     tc_fence_before();

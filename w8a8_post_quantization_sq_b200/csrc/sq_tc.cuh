@@ -36,11 +36,12 @@ __device__ __forceinline__ bool wait_fast(uint32_t bar, uint32_t parity, volatil
 }
 
 // Short bounded wait used while draining after an abort (ignores the flag).
-static __device__ __noinline__ void wait_drain(uint32_t bar, uint32_t parity) {
+__device__ __forceinline__ void wait_drain_inline(uint32_t bar, uint32_t parity) {
     const uint64_t t0 = global_ns();
     while (!mbar_try_wait(bar, parity))
         if (global_ns() - t0 > kTimeoutNs / 4) return;
 }
+static __device__ __noinline__ void wait_drain(uint32_t bar, uint32_t parity) { wait_drain_inline(bar, parity); }
 
 // Tile (x = k, y = row) of problem z of a 3-D [batch, rows, K] int8 tensor
 // into this CTA's shared memory. CG = 2: the completion is counted on the

@@ -42,8 +42,10 @@ __device__ __forceinline__ uint64_t global_ns() {
 // and records `code` in the status word (read on the host by
 // sq_workspace_status). Never traps: the caller drains its own work and
 // returns.
-static __device__ __noinline__ bool wait_bounded_ns(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* status,
-                                             int code, uint64_t timeout_ns) {
+// (In a function of its own below; inline for kernels that deal out registers
+// with setmaxnreg, which leaves no room for calls.)
+__device__ __forceinline__ bool wait_bounded_inline(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* status,
+                                                    int code, uint64_t timeout_ns) {
     if (mbar_try_wait(bar, parity)) return true;
     const uint64_t t0 = global_ns();
     for (uint32_t n = 1;; ++n) {
@@ -55,6 +57,10 @@ static __device__ __noinline__ bool wait_bounded_ns(uint32_t bar, uint32_t parit
             return false;
         }
     }
+}
+static __device__ __noinline__ bool wait_bounded_ns(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* status,
+                                             int code, uint64_t timeout_ns) {
+    return wait_bounded_inline(bar, parity, abort_flag, status, code, timeout_ns);
 }
 
 }  // namespace sq
