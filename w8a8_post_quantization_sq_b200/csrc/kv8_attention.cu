@@ -208,7 +208,7 @@ kv8_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
             // eight tiles' block numbers are on their way meanwhile
             auto block_of = [&](int t0) {
                 const int key = t0 * kTile + lane * kSub;
-                return key < vis ? __ldg(row + key / a.block) : -1;
+                return key < vis ? __ldg(row + (key >> a.block_log2)) : -1;
             };
             int blk_next = block_of(w.k0);
             for (int t0 = w.k0; ok && t0 < last; t0 += 8) {
@@ -650,6 +650,7 @@ extern "C" sq_status_t sq_kv8_attention(const void* Q, sq_dtype_t dt, int64_t T,
     a.Hkv = (int)Hkv;
     a.G = (int)(Hq / Hkv);
     a.block = (int)block;
+    a.block_log2 = block == 16 ? 4 : block == 32 ? 5 : block == 64 ? 6 : 7;
     a.box = (int)(block < sq::kTile ? block : sq::kTile);
     a.max_blocks = (int)max_blocks;
     a.causal = causal != 0;

@@ -17,9 +17,14 @@
 //                      rescales O and writes Y
 //   warps 8..11        int8 K and V tiles to fp16 tiles (128-byte swizzle): 128
 //                      x D codes are converted once for 256 rows
-//   warp 12            TMA of the int8 tiles, warp 13 the MMAs (14, 15 idle)
+//   warp 12            TMA of the int8 tiles
+//   warp 13            the MMAs
+//   warp 14            the CTA's items, worked out ahead and left in a ring
 // Items are (sequence, 256 rows, head), the last rows of every sequence first (they
 // see the most keys), dealt to the CTAs forth and back.
+// The loops are rolled where the roles' code together would leave the
+// instruction cache (unrolled throughout it took 120 KB, and a change of items
+// 15,000 cycles of instruction fetches).
 // What bounds it: 128 x 128 scores take 512 cycles of the tensor core for each
 // product at D = 128 and 1024 of the exponential unit, two tiles 2048 of either.
 // Every wait is bounded (about 2 s), code 0x9E1 + role in the status word.
@@ -35,11 +40,11 @@ namespace {
 constexpr int kKeys = 128;
 constexpr int kTileRows = 128;
 constexpr int kItemRows = 2 * kTileRows;
-constexpr int kRaw = 3, kF16 = 3;  // ring stages: int8 tiles, fp16 tiles
+constexpr int kRaw = 2, kF16 = 4;  // ring stages: int8 tiles, fp16 tiles
 constexpr int kThreadsP = 16 * 32;
 // Registers per thread: 128 at launch, dealt out again by warpgroup (two softmax
 // groups, conversion, TMA and MMA).
-constexpr int kRegsSoftmax = 160, kRegsConvert = 96, kRegsIssue = 96;
+constexpr int kRegsSoftmax = 168, kRegsConvert = 96, kRegsIssue = 80;
 static_assert(2 * kRegsSoftmax + kRegsConvert + kRegsIssue <= 4 * 128, "more registers than the block was launched with");
 
 template <int D>
@@ -51,10 +56,12 @@ struct PCfg {
     static constexpr uint32_t F_OFF = Q_OFF + 2 * TILE;
     static constexpr uint32_t R_OFF = F_OFF + kF16 * TILE;
     static constexpr uint32_t BAR_OFF = R_OFF + kRaw * RAW;
-    // raw_full[3], raw_empty[3], f_full[3], f_empty[3], q_ready[2], s_full[2], p_full[2], o_full[2], drain
-    static constexpr uint32_t NBAR = 2 * kRaw + 2 * kF16 + 9;
-    static constexpr uint32_t MISC_OFF = BAR_OFF + NBAR * 8;  // tmem base, abort flag
-    static constexpr uint32_t SMEM_ALLOC = MISC_OFF + 16 + 1024;
+    // raw_full[R], raw_empty[R], f_full[F], f_empty[F], q_ready[2], s_full[2], p_full[2], o_full[2], drain
+    // item_full[2], item_empty[2]
+    static constexpr uint32_t NBAR = 2 * kRaw + 2 * kF16 + 9 + 4;
+    static constexpr uint32_t MISC_OFF = BAR_OFF + (NBAR + 1) / 2 * 16;  // tmem base, abort flag
+    static constexpr uint32_t ITEM_OFF = MISC_OFF + 16;                  // Item[2]
+    static constexpr uint32_t SMEM_ALLOC = ITEM_OFF + 2 * 64 + 1024;
     static_assert(SMEM_ALLOC <= 232448, "over the 227 KB of shared memory a block may use");
     static constexpr uint32_t O_COL = 256;  // O of tile x at O_COL + x * D, S and P at x * 128
     // fp16 x fp16 -> fp32, M = 128: N = 128 keys, both K-major; N = D, V MN-major (bit 16)
@@ -101,37 +108,41 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t* r) {
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+// One item, as the scheduling warp leaves it for the others.
+struct Item {
+    int64_t lo;    // first new token of the sequence
+    int b, h, r0;  // sequence (-1: no more items), head, first row
+    int n, len;    // new tokens and length of the sequence
+    int tiles[2];  // key tiles of each row tile
+    int vis;       // keys that the item's last row sees
+};
+
 // The CTA's items in turn. Level k of the order holds the k-th row block from
-// the end of every sequence that has one, for every head. Every warp walks the
-// items together (32 sequences a look).
+// the end of every sequence that has one, for every head. One warp walks them
+// (32 sequences a look).
 struct Items {
     int64_t before, count;  // items of the levels before `level`, and of it
     int level, round;
-    Seq s;
-    int b, h, r0;
-    int tiles[2];  // key tiles of each row tile
-    int vis;       // keys that the item's last row sees
+    int mine;  // row blocks of sequence `lane`
 
-    // row blocks of sequence i
-    __device__ __forceinline__ int blocks_of(const AttnArgs& a, int i) const {
+    // row blocks of sequence i (the first 32 sequences' are kept)
+    __device__ __forceinline__ int blocks_of(const AttnArgs& a, int i, bool kept = true) const {
+        if (kept && i < 32) return mine;
         if (i >= a.B) return 0;
         const Seq t = seq_of<kItemRows, kKeys>(a, i);
         return (int64_t)t.n * a.G > a.row_limit ? t.rt : 0;
     }
     __device__ __forceinline__ void look(const AttnArgs& a, int lane) {
         int n = 0;
+#pragma unroll 1
         for (int base = 0; base < a.B; base += 32)
             n += __popc(__ballot_sync(0xffffffffu, blocks_of(a, base + lane) > level));
         count = (int64_t)n * a.Hkv;
     }
-    __device__ __forceinline__ void init(const AttnArgs& a, int lane) {
-        before = 0;
-        level = round = 0;
-        look(a, lane);
-    }
-    __device__ __forceinline__ bool next(const AttnArgs& a, int lane) {
+    __device__ __forceinline__ bool next(const AttnArgs& a, int lane, Item& it) {
         const int64_t at = (int64_t)round * gridDim.x + ((round & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
         ++round;
+#pragma unroll 1
         while (at >= before + count) {
             if (count == 0) return false;
             before += count;
@@ -140,28 +151,33 @@ struct Items {
         }
         const int idx = (int)(at - before);
         int nth = idx / a.Hkv;  // the nth sequence with a block of this level
-        h = idx - nth * a.Hkv;
+        it.h = idx - nth * a.Hkv;
+#pragma unroll 1
         for (int base = 0;; base += 32) {
             const int blocks = blocks_of(a, base + lane);
             const unsigned has = __ballot_sync(0xffffffffu, blocks > level);
             const int n = __popc(has);
             if (nth < n) {
                 unsigned left = has;
+#pragma unroll 1
                 while (nth-- > 0) left &= left - 1;
                 const int l = __ffs(left) - 1;
-                b = base + l;
-                r0 = (__shfl_sync(0xffffffffu, blocks, l) - 1 - level) * kItemRows;
+                it.b = base + l;
+                it.r0 = (__shfl_sync(0xffffffffu, blocks, l) - 1 - level) * kItemRows;
                 break;
             }
             nth -= n;
         }
-        s = seq_of<kItemRows, kKeys>(a, b);
+        const Seq s = seq_of<kItemRows, kKeys>(a, it.b);
+        it.lo = s.lo;
+        it.n = s.n;
+        it.len = s.len;
         const int rows = s.n * a.G;
-        vis = seen_by(a, s, min(r0 + kItemRows, rows) - 1);
-#pragma unroll
+        it.vis = seen_by(a, s, min(it.r0 + kItemRows, rows) - 1);
+#pragma unroll 1
         for (int x = 0; x < 2; ++x) {
-            const int f = r0 + x * kTileRows;
-            tiles[x] = f < rows ? (seen_by(a, s, min(f + kTileRows, rows) - 1) + kKeys - 1) / kKeys : 0;
+            const int f = it.r0 + x * kTileRows;
+            it.tiles[x] = f < rows ? (seen_by(a, s, min(f + kTileRows, rows) - 1) + kKeys - 1) / kKeys : 0;
         }
         return true;
     }
@@ -186,6 +202,8 @@ kv8_prefill_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_const
     auto p_full = [&](int x) { return bar1 + 8u * (4 + x); };
     auto o_full = [&](int x) { return bar1 + 8u * (6 + x); };
     const uint32_t drain_bar = bar1 + 8u * 8;
+    auto item_full = [&](int s) { return bar1 + 8u * (9 + s); };
+    auto item_empty = [&](int s) { return bar1 + 8u * (11 + s); };
     uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + C::MISC_OFF);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::MISC_OFF + 4);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -203,6 +221,8 @@ kv8_prefill_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_const
             mbar_init(s_full(x), 1);
             mbar_init(p_full(x), 4);
             mbar_init(o_full(x), 1);
+            mbar_init(item_full(x), 1);
+            mbar_init(item_empty(x), 14);  // warps 0..13
         }
         mbar_init(drain_bar, 1);
         *abort_flag = 0;
@@ -221,11 +241,21 @@ kv8_prefill_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_const
     pdl_wait();
     pdl_trigger();
     auto wait = [&](uint32_t bar, uint32_t parity, int code) {
-        return wait_bounded_inline(bar, parity, abort_flag, a.status, code, kTimeoutNs);
+        return wait_suspended(bar, parity, abort_flag, a.status, code, kTimeoutNs);
     };
-    Items it;
-    it.init(a, lane);
     bool ok = true;
+    int is = 0;  // items taken from the ring
+    // the next item (whole warps; false when there are no more)
+    auto take_item = [&](Item& it) {
+        ok = wait(item_full(is & 1), (uint32_t)(is >> 1) & 1u, 0x9E9);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) return false;
+        it = *reinterpret_cast<const Item*>(smem + C::ITEM_OFF + (is & 1) * 64);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(item_empty(is & 1));
+        ++is;
+        return it.b >= 0;
+    };
     if (warp < 8) {
         // ------------------------------------------------------ softmax
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
@@ -234,23 +264,35 @@ kv8_prefill_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_const
         const uint32_t quarter = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t t_s = tmem + quarter + (uint32_t)(x * 128), t_o = tmem + quarter + C::O_COL + (uint32_t)(x * D);
         uint32_t s_phase = 0, o_phase = 0;
-        while (ok && it.next(a, lane)) {
-            const int rows = it.s.n * a.G;
+        // this thread's row of the item, and its q on the way
+        Item it = {};
+        bool live;
+        int vis;  // keys that the row sees (rows past the end: all, computed and not written)
+        T* y;
+        uint4 w[D / 8];
+        auto fetch = [&]() {
+            const int rows = it.n * a.G;
             const int r = it.r0 + x * kTileRows + row;
-            const bool live = r < rows;
+            live = r < rows;
             const int i = live ? r / a.G : 0;
-            const int64_t at = (it.s.lo + i) * 1;  // token
             const int64_t head = (int64_t)(it.h * a.G + (live ? r - i * a.G : 0)) * D;
+            const T* q = static_cast<const T*>(a.Q) + (it.lo + i) * a.ldq + head;
+            y = static_cast<T*>(a.Y) + (it.lo + i) * a.ldy + head;
+            vis = !live ? INT_MAX : a.causal ? max(min(it.len - it.n + i + 1, it.len), 0) : it.len;
+#pragma unroll
+            for (int e = 0; e < D / 8; ++e) w[e] = live ? ldg_nc_v4(q + 8 * e) : make_uint4(0, 0, 0, 0);
+        };
+        bool more = take_item(it);
+        if (more) fetch();
+#pragma unroll 1
+        while (more) {
             // Q: scaled by a power of two per row to [1, 2), the score scale's
             // sign in it, as fp16 to the swizzled tile
             float crow;
             {
-                const T* q = static_cast<const T*>(a.Q) + at * a.ldq + head;
-                uint4 w[D / 8];
                 uint32_t m2 = 0;
 #pragma unroll
                 for (int e = 0; e < D / 8; ++e) {
-                    w[e] = live ? ldg_nc_v4(q + 8 * e) : make_uint4(0, 0, 0, 0);
                     m2 = __vmaxu2(m2, __vmaxu2(w[e].x & 0x7fff7fffu, w[e].y & 0x7fff7fffu));
                     m2 = __vmaxu2(m2, __vmaxu2(w[e].z & 0x7fff7fffu, w[e].w & 0x7fff7fffu));
                 }
@@ -274,28 +316,30 @@ kv8_prefill_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_const
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(q_ready(x));
-            // (rows past the sequence's end are computed unmasked and not written)
-            const int vis = live ? seen_by(a, it.s, r) : INT_MAX;
             const int32_t* table = a.table + (int64_t)it.b * a.ldb;
-            // lane e < 8 looks after the scales of keys 16 e .. of a tile, one tile ahead
-            auto scales_of = [&](int j) {
-                float kq = __uint_as_float(0x7fffffffu), vq = kq;
+            // lane e < 8 looks after the scales of keys 16 e .. of a tile: the block
+            // number two tiles ahead, the scales one
+            auto block_of = [&](int j) {
                 const int key = j * kKeys + (lane & 7) * 16;
-                if (key < it.vis) {
-                    const int64_t blk = __ldg(table + key / a.block);
-                    if (blk >= 0 && blk < a.num_blocks) {
-                        kq = __ldg(a.kqs + blk * a.Hkv + it.h);
-                        vq = __ldg(a.vqs + blk * a.Hkv + it.h);
-                    }
+                return key < it.vis ? __ldg(table + (key >> a.block_log2)) : -1;
+            };
+            auto scales_of = [&](int blk) {
+                float2 s = make_float2(__uint_as_float(0x7fffffffu), __uint_as_float(0x7fffffffu));
+                if (blk >= 0 && blk < a.num_blocks) {
+                    s.x = __ldg(a.kqs + (int64_t)blk * a.Hkv + it.h);
+                    s.y = __ldg(a.vqs + (int64_t)blk * a.Hkv + it.h);
                 }
-                return make_float2(kq, vq);
+                return s;
             };
             const int tiles = it.tiles[x];
             float m = -INFINITY, l = 0.0f;
-            float2 next = scales_of(0);
+            int next_blk = block_of(1);
+            float2 next = scales_of(block_of(0));
+#pragma unroll 1
             for (int j = 0; j < tiles; ++j) {
                 const float my_k = __frcp_rn(next.x), my_v = next.y, my_lv = -__log2f(next.y);
-                if (j + 1 < tiles) next = scales_of(j + 1);
+                next = scales_of(next_blk);
+                next_blk = block_of(j + 2);
                 ok = wait(s_full(x), s_phase, 0x9E1);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
@@ -305,47 +349,44 @@ kv8_prefill_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_const
                 const bool masked = __any_sync(0xffffffffu, key0 + kKeys > vis);
                 // per 16 keys: score factor and -log2 of the V scale; of keys that
                 // this row does not see nothing is taken, whatever their scales
-                float f[8], lv[8];
-#pragma unroll
-                for (int q = 0; q < 8; ++q) {
-                    f[q] = crow * __shfl_sync(0xffffffffu, my_k, q);
-                    lv[q] = __shfl_sync(0xffffffffu, my_lv, q);
-                    if (key0 + 16 * q >= vis) f[q] = 1.0f, lv[q] = 0.0f;
-                }
+                auto factors = [&](int k, float& f, float& lv) {
+                    f = crow * __shfl_sync(0xffffffffu, my_k, k);
+                    lv = __shfl_sync(0xffffffffu, my_lv, k);
+                    if (key0 + 16 * k >= vis) f = 1.0f, lv = 0.0f;
+                };
+                uint32_t s[64];
                 float tm = -INFINITY;
-                auto mask = [&](uint32_t* s, int c) {
-                    if (masked)
+#pragma unroll 1
+                for (int c = 0; c < 2; ++c) {
+                    // the maximum over 64 keys (as a tree: a chain of 16 waits for
+                    // every one of them)
+                    tmem_ld32_async(t_s + c * 64, s);
+                    tmem_ld32_async(t_s + c * 64 + 32, s + 32);
+                    tmem_wait(s);
+                    tmem_wait(s + 32);
+                    if (masked) {
 #pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            if (key0 + 32 * c + e >= vis) s[e] = 0xff800000u;
-                };
-                auto top = [&](const uint32_t* s, int c) {
+                        for (int e = 0; e < 64; ++e)
+                            if (key0 + 64 * c + e >= vis) s[e] = 0xff800000u;
+                        // (read again below)
 #pragma unroll
-                    for (int q = 0; q < 2; ++q) {
-                        float v = __uint_as_float(s[16 * q]);
-#pragma unroll
-                        for (int e = 1; e < 16; ++e) v = fmaxf(v, __uint_as_float(s[16 * q + e]));
-                        tm = fmaxf(tm, fmaf(v, f[2 * c + q], lv[2 * c + q]));
+                        for (int e = 0; e < 4; ++e) tmem_st16(t_s + c * 64 + 16 * e, s + 16 * e);
+                        tmem_wait_st();
                     }
-                };
-                // the maximum: chunks 0 and 1, then 2 and 3, which stay
-                uint32_t sa[32], sb[32];
-                tmem_ld32_async(t_s, sa);
-                tmem_ld32_async(t_s + 32, sb);
-                tmem_wait(sa);
-                tmem_wait(sb);
-                mask(sa, 0);
-                mask(sb, 1);
-                top(sa, 0);
-                top(sb, 1);
-                tmem_ld32_async(t_s + 64, sa);
-                tmem_ld32_async(t_s + 96, sb);
-                tmem_wait(sa);
-                tmem_wait(sb);
-                mask(sa, 2);
-                mask(sb, 3);
-                top(sa, 2);
-                top(sb, 3);
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        float v[8], f, lv;
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            v[e] = fmaxf(__uint_as_float(s[16 * q + e]), __uint_as_float(s[16 * q + 8 + e]));
+#pragma unroll
+                        for (int e = 4; e > 0; e >>= 1)
+#pragma unroll
+                            for (int z = 0; z < e; ++z) v[z] = fmaxf(v[z], v[z + e]);
+                        factors(4 * c + q, f, lv);
+                        tm = fmaxf(tm, fmaf(v[0], f, lv));
+                    }
+                }
                 const bool move = tm > m + kSlack;
                 if (__any_sync(0xffffffffu, move)) {
                     const float to = move ? tm : m;
@@ -365,42 +406,48 @@ kv8_prefill_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_const
                     }
                 }
                 const float mu = m == -INFINITY ? 0.0f : m;
-                // P of chunk c goes to the first half of the chunk's own columns
-                auto weights = [&](const uint32_t* s, int c) {
-                    uint32_t p[16];
+                // weights: P of 32 keys goes to the first half of their own columns
+#pragma unroll 1
+                for (int c = 0; c < 2; ++c) {
+                    tmem_ld32_async(t_s + c * 64, s);
+                    tmem_ld32_async(t_s + c * 64 + 32, s + 32);
+                    tmem_wait(s);
+                    tmem_wait(s + 32);
 #pragma unroll
-                    for (int q = 0; q < 2; ++q) {
-                        const int k = 2 * c + q;
-                        const uint64_t f2 = pk2(f[k], f[k]), c2 = pk2(lv[k] - mu, lv[k] - mu);
-                        uint64_t sum2 = 0;
+                    for (int hf = 0; hf < 2; ++hf) {
+                        uint32_t p[16];
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            float p0, p1;
-                            upk2(fma2(pk2(__uint_as_float(s[16 * q + 2 * e]), __uint_as_float(s[16 * q + 2 * e + 1])), f2,
-                                      c2),
-                                 p0, p1);
-                            p0 = ex2(p0);
-                            p1 = ex2(p1);
-                            sum2 = e == 0 ? pk2(p0, p1) : add2(sum2, pk2(p0, p1));
-                            p[8 * q + e] = pack_half2(p0, p1);
+                        for (int q = 0; q < 2; ++q) {
+                            const int k = 4 * c + 2 * hf + q;
+                            const uint32_t* sk = s + 32 * hf + 16 * q;
+                            float f, lv;
+                            factors(k, f, lv);
+                            const uint64_t f2 = pk2(f, f), c2 = pk2(lv - mu, lv - mu);
+                            uint64_t w2[8];
+#pragma unroll
+                            for (int e = 0; e < 8; ++e)
+                                w2[e] = fma2(pk2(__uint_as_float(sk[2 * e]), __uint_as_float(sk[2 * e + 1])), f2, c2);
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) {
+                                float p0, p1;
+                                upk2(w2[e], p0, p1);
+                                p0 = ex2(p0);
+                                p1 = ex2(p1);
+                                w2[e] = pk2(p0, p1);
+                                p[8 * q + e] = pack_half2(p0, p1);
+                            }
+#pragma unroll
+                            for (int e = 4; e > 0; e >>= 1)
+#pragma unroll
+                                for (int z = 0; z < e; ++z) w2[z] = add2(w2[z], w2[z + e]);
+                            float a0, a1;
+                            upk2(w2[0], a0, a1);
+                            const float vq = __shfl_sync(0xffffffffu, my_v, k);
+                            l = fmaf(a0 + a1, key0 + 16 * k < vis ? vq : 0.0f, l);
                         }
-                        float a0, a1;
-                        upk2(sum2, a0, a1);
-                        const float vq = __shfl_sync(0xffffffffu, my_v, k);
-                        l = fmaf(a0 + a1, key0 + 16 * k < vis ? vq : 0.0f, l);
+                        tmem_st16(t_s + c * 64 + hf * 32, p);
                     }
-                    tmem_st16(t_s + c * 32, p);
-                };
-                weights(sa, 2);
-                tmem_ld32_async(t_s, sa);
-                weights(sb, 3);
-                tmem_ld32_async(t_s + 32, sb);
-                tmem_wait(sa);
-                tmem_wait(sb);
-                mask(sa, 0);
-                mask(sb, 1);
-                weights(sa, 0);
-                weights(sb, 1);
+                }
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
@@ -408,7 +455,12 @@ kv8_prefill_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_const
             }
             if (!ok) break;
             const float inv = (m == -INFINITY && l == 0.0f) ? 0.0f : __frcp_rn(l);
-            T* y = static_cast<T*>(a.Y) + at * a.ldy + head;
+            T* const out = y;
+            const bool write = live;
+            // the next item's q is fetched while this one's last product runs
+            more = take_item(it);
+            if (!ok) break;
+            if (more) fetch();
             if (tiles > 0) {
                 ok = wait(o_full(x), o_phase, 0x9E2);
                 ok = __all_sync(0xffffffffu, ok);
@@ -417,23 +469,23 @@ kv8_prefill_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_const
                 tc_fence_after();
             }
 #pragma unroll 1
-            for (int c = 0; c < D / 32; ++c) {
-                uint32_t s[32];
+            for (int c = 0; c < D / 16; ++c) {
+                uint32_t s[16];
                 if (tiles > 0) {
-                    tmem_ld32(t_o + c * 32, s);
+                    tmem_ld16(t_o + c * 16, s);
                 } else {
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) s[e] = 0u;
+                    for (int e = 0; e < 16; ++e) s[e] = 0u;
                 }
-                if (live) {
+                if (write) {
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
+                    for (int q = 0; q < 2; ++q) {
                         uint32_t p[4];
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
                             p[e] = (uint32_t)to16<T>(__uint_as_float(s[8 * q + 2 * e]) * inv) |
                                    ((uint32_t)to16<T>(__uint_as_float(s[8 * q + 2 * e + 1]) * inv) << 16);
-                        *reinterpret_cast<uint4*>(y + c * 32 + 8 * q) = make_uint4(p[0], p[1], p[2], p[3]);
+                        *reinterpret_cast<uint4*>(out + c * 16 + 8 * q) = make_uint4(p[0], p[1], p[2], p[3]);
                     }
                 }
             }
@@ -444,8 +496,11 @@ kv8_prefill_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_const
         const int t = threadIdx.x - 256;
         int rs = 0, fs = 0;
         uint32_t rp = 0, fp = 0;
-        while (ok && it.next(a, lane)) {
+        Item it;
+#pragma unroll 1
+        while (ok && take_item(it)) {
             const int n = 2 * max(it.tiles[0], it.tiles[1]);
+#pragma unroll 1
             for (int j = 0; ok && j < n; ++j) {
                 ok = wait(raw_full(rs), rp, 0x9E3) &&
                      wait(f_empty(fs), fp ^ 1u, 0x9E4);
@@ -454,7 +509,7 @@ kv8_prefill_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_const
                 const uint8_t* src = smem + C::R_OFF + rs * C::RAW;
                 uint8_t* dst = smem + C::F_OFF + fs * C::TILE;
                 constexpr int UPR = D / 16;  // 16-code units per key
-#pragma unroll
+#pragma unroll 4
                 for (int k = 0; k < kKeys * UPR / 128; ++k) {
                     const int unit = k * 128 + t;
                     const int key = unit / UPR, u = unit % UPR;
@@ -492,25 +547,29 @@ kv8_prefill_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_const
         int rs = 0;
         uint32_t rp = 0, issued = 0, issued_phase = 0;
         const int box = a.box, per_box = box / 16;
-        while (ok && it.next(a, lane)) {
+        Item it;
+#pragma unroll 1
+        while (ok && take_item(it)) {
             const int n = max(it.tiles[0], it.tiles[1]);
             const int32_t* table = a.table + (int64_t)it.b * a.ldb;
             // lane e looks after part e % 8 (16 keys) of tile j0 + e / 8
             auto block_of = [&](int j0) {
                 const int key = j0 * kKeys + lane * 16;
-                const int blk = key < it.vis ? __ldg(table + key / a.block) : -1;
+                const int blk = key < it.vis ? __ldg(table + (key >> a.block_log2)) : -1;
                 return blk >= 0 && blk < a.num_blocks ? blk : -1;
             };
             int next = block_of(0);
+#pragma unroll 1
             for (int j0 = 0; ok && j0 < n; j0 += 4) {
                 const int blk = next;
                 if (j0 + 4 < n) next = block_of(j0 + 4);
                 const int y = it.h * a.block + ((j0 * kKeys + lane * 16) & (a.block - 1));
+#pragma unroll 1
                 for (int j = j0; ok && j < min(j0 + 4, n); ++j) {
                     const int part = lane - (j - j0) * 8;
                     const bool copy = part >= 0 && part < 8 && blk >= 0 && part % per_box == 0;
                     const int boxes = __popc(__ballot_sync(0xffffffffu, copy));
-#pragma unroll
+#pragma unroll 1
                     for (int v = 0; v < 2; ++v) {
                         ok = wait(raw_empty(rs), rp ^ 1u, 0x9E5);
                         ok = __all_sync(0xffffffffu, ok);
@@ -535,7 +594,9 @@ kv8_prefill_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_const
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
         int fs = 0;  // stage of the next fp16 tile in the order K0 V0 K1 V1 ...
         uint32_t fp = 0, q_phase = 0, p_phase[2] = {0, 0};
-        while (ok && it.next(a, lane)) {
+        Item it;
+#pragma unroll 1
+        while (ok && take_item(it)) {
             if (lane == 0) {
                 const int n0 = it.tiles[0], n1 = it.tiles[1], n = max(n0, n1);
                 auto take = [&](int& stage) {  // waits for the next fp16 tile
@@ -558,21 +619,16 @@ kv8_prefill_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_const
                      wait(q_ready(1), q_phase, 0x9E7);
                 tc_fence_after();
                 int ks = 0, vs = 0;
-                if (ok && n > 0) {
-                    ok = take(ks);
-                    if (ok) {
-                        if (n0 > 0) score(0, ks);
-                        if (n1 > 0) score(1, ks);
-                        umma_commit<1>(f_empty(ks));
-                    }
-                }
-                for (int j = 0; ok && j < n; ++j) {
-                    ok = take(vs);
+                // step j: the products with V of tile j (from 0), then the scores of tile j + 1
+#pragma unroll 1
+                for (int j = -1; ok && j < n; ++j) {
+                    if (j >= 0) ok = take(vs);
                     const bool more = j + 1 < n;
                     bool have_k = false;
+#pragma unroll 1
                     for (int x = 0; ok && x < 2; ++x) {
                         const int nx = x ? n1 : n0;
-                        if (j < nx) {
+                        if (j >= 0 && j < nx) {
                             ok = wait(p_full(x), p_phase[x], 0x9E8);
                             if (!ok) break;
                             p_phase[x] ^= 1u;
@@ -584,6 +640,7 @@ kv8_prefill_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_const
                                         sdesc_mn(vb + k * 16 * 128, C::HALF), C::IDESC_O, (j != 0 || k != 0) ? 1u : 0u);
                             if (j + 1 == nx) umma_commit<1>(o_full(x));
                         }
+                        if (x == 1 && j >= 0) umma_commit<1>(f_empty(vs));  // both products with V are issued
                         if (more && !have_k) {
                             ok = take(ks);
                             have_k = true;
@@ -591,7 +648,6 @@ kv8_prefill_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_const
                         if (ok && j + 1 < nx) score(x, ks);
                     }
                     if (!ok) break;
-                    umma_commit<1>(f_empty(vs));
                     if (more) umma_commit<1>(f_empty(ks));
                 }
                 q_phase ^= 1u;
@@ -603,7 +659,28 @@ kv8_prefill_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_const
             wait_drain_inline(drain_bar, 0);
         }
     } else {
+        // ------------------------------------------------------ items
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
+        if (warp == 14) {
+            Items list;
+            list.before = 0;
+            list.level = list.round = 0;
+            list.mine = list.blocks_of(a, lane, false);
+            list.look(a, lane);
+            bool more = true;
+#pragma unroll 1
+            for (int n = 0; more; ++n) {
+                Item it;
+                more = list.next(a, lane, it);
+                if (!more) it.b = -1;
+                ok = wait(item_empty(n & 1), ((uint32_t)(n >> 1) & 1u) ^ 1u, 0x9EA);
+                if (!__all_sync(0xffffffffu, ok)) break;
+                if (lane == 0) {
+                    *reinterpret_cast<Item*>(smem + C::ITEM_OFF + (n & 1) * 64) = it;
+                    mbar_arrive(item_full(n & 1));
+                }
+            }
+        }
     }
     __syncwarp();
     tc_fence_before();

@@ -42,7 +42,7 @@ struct AttnArgs {
     const int32_t* table;
     const float* kqs;
     const float* vqs;
-    int B, Hkv, G, block, box, max_blocks, causal;
+    int B, Hkv, G, block, block_log2, box, max_blocks, causal;
     int64_t row_limit;  // sequences of more rows (new tokens x G) than this are the prompt kernel's
     float scale;
     int* status;
