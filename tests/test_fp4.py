@@ -141,7 +141,7 @@ def check_quant(x, fmt, s=None, weight=False, static=None):
 @pytest.mark.gpu
 @pytest.mark.parametrize("fmt", FMTS)
 @pytest.mark.parametrize("dt", DTYPES)
-@pytest.mark.parametrize("M,K", [(1, 32), (3, 64), (130, 96), (129, 4096), (7, 1056), (5, 12288), (2, 40000), (33, 544)])
+@pytest.mark.parametrize("M,K", [(1, 32), (3, 64), (130, 96), (129, 4096), (7, 1056), (5, 12288), (2, 40000), (33, 544), (2000, 2048), (700, 20480), (3, 49152), (3, 65536)])
 def test_quantise(M, K, dt, fmt):
     check_quant(data(M, K, dt), fmt)
 
