@@ -341,7 +341,7 @@ def test_gemm_workspace_and_repeats():
             check_gemm(y, xv, wv, None, K)
             ys.append(y)
         assert torch.equal(ys[0], ys[1])
-        assert int(ws[256 : 256 + 8192].sum()) == 0  # counters are zero again
+        assert int(ws.sum()) == 0
         sq.sq_workspace_status(ws)
 
 

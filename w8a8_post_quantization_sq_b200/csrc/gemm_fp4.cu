@@ -21,9 +21,11 @@
 //     scales' two sets of 48 (24) columns exceed the 512 of tensor memory, so the
 //     accumulators share 96 (48): the epilogue reads the shared columns first
 //     and hands them back, and the next tile's MMAs start while the rest is read;
-//   - few tiles (decode batches): the k-loop of each 128 x 128 tile is cut into
-//     equal parts, one CTA each; partial sums are parked in the workspace and
-//     added in part order by the CTA that arrives last.
+//   - few tiles (decode batches): a kernel of its own, one 128 x 128 tile (or one
+//     part of its k-loop) per CTA, two CTAs per SM; the parts of a tile are a
+//     cluster, which adds them up through its shared memory, in part order.
+//     (Parked in global memory and counted by atomics, the parts cost 2.5 us
+//     more: 16 x 4096 x 4096 9.9 us, so 6.2 us.)
 // Every wait is bounded (about 2 s), code 0x8E1 + role in the status word.
 #include <cstring>
 #include <type_traits>
@@ -91,7 +93,7 @@ struct Cfg {
 struct Params {
     int M, N, K;
     int num_m, num_n, num_kb;
-    int tiles, splits;
+    int tiles;
     int group_m;
     int vec_store, tma_store;
     const float* qs_x;
@@ -101,9 +103,6 @@ struct Params {
     void* Y;
     int64_t ldy;
     int* status;
-    int* cnt;      // [tiles][kEpiWarps] parts counted in (zero between launches)
-    float* part;   // [CTA][kEpiWarps][NCH][8][32] float4
-    int cnt_bytes;
 };
 
 __device__ __forceinline__ void tile_coords(int tile, const Params& p, int bm, int bn, int& m0, int& n0) {
@@ -319,10 +318,8 @@ gemm_fp4_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constan
     const uint32_t tmem_base = *tmem_holder;
     pdl_wait();
     pdl_trigger();
-    if (p.splits > 1 && blockIdx.x == 0 && threadIdx.x == 0) p.status[3] = p.cnt_bytes;
 
-    // this CTA's (or pair's) items: tile w / splits, part w % splits of its k-loop
-    const int first = blockIdx.x / CG, step = gridDim.x / CG, items = p.tiles * p.splits;
+    const int first = blockIdx.x / CG, step = gridDim.x / CG, items = p.tiles;  // this CTA's (or pair's) tiles
     if (warp == 0) {
         if (lane == 0) {
             // ---------------------------------------------------- TMA producer
@@ -330,15 +327,12 @@ gemm_fp4_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constan
             uint32_t phase = 0, issued = 0, issued_phase = 0;
             bool ok = true;
             for (int w = first; ok && w < items; w += step) {
-                const int tile = w / p.splits, part = w - tile * p.splits;
-                const int k0 = (int)((int64_t)part * p.num_kb / p.splits);
-                const int k1 = (int)((int64_t)(part + 1) * p.num_kb / p.splits);
                 int m0, n0;
-                tile_coords(tile, p, BM * CG, BN, m0, n0);
+                tile_coords(w, p, BM * CG, BN, m0, n0);
                 const int gn = n0 / 128;
                 m0 += (int)rank * BM;
                 n0 += (int)rank * (BN / CG);
-                for (int kb = k0; kb < k1; ++kb) {
+                for (int kb = 0; kb < p.num_kb; ++kb) {
                     if (!wait_fast(empty_bar(stage), phase ^ 1u, abort_flag, p.status, 0x8E1)) {
                         ok = false;
                         break;
@@ -372,9 +366,6 @@ gemm_fp4_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constan
             uint32_t phase = 0, set = 0;
             bool ok = true;
             for (int w = first; ok && w < items; w += step, ++local) {
-                const int part = w - w / p.splits * p.splits;
-                const int k0 = (int)((int64_t)part * p.num_kb / p.splits);
-                const int k1 = (int)((int64_t)(part + 1) * p.num_kb / p.splits);
                 const int acc = local & 1;
                 // accumulators that share columns: the previous tile's shared
                 // columns (and all of the tile before it) have been read; else
@@ -387,7 +378,7 @@ gemm_fp4_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constan
                 }
                 tc_fence_after();
                 const uint32_t d_tmem = tmem_base + (acc ? C::ACC1 : 0u);
-                for (int kb = k0; kb < k1; ++kb) {
+                for (int kb = 0; kb < p.num_kb; ++kb) {
                     if (!wait_fast(full_bar(stage), phase, abort_flag, p.status, 0x8E3) ||
                         !wait_fast(sready_bar(stage), phase, abort_flag, p.status, 0x8E5)) {
                         ok = false;
@@ -406,7 +397,7 @@ gemm_fp4_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constan
                         const int c = FMT == SQ_NVFP4 ? k : k >> 1;       // scale tile of this MMA
                         const int sf = FMT == SQ_NVFP4 ? 0 : (k & 1) * 2;  // first byte of its words
                         umma_fp4<FMT, CG>(d_tmem, sdesc(a_addr + k * (UMMA_K / 2)), sdesc(b_addr + k * (UMMA_K / 2)),
-                                          C::idesc(sf), sfa + c * 4, sfb + c * C::NG * 4, (kb != k0 || k != 0) ? 1u : 0u);
+                                          C::idesc(sf), sfa + c * 4, sfb + c * C::NG * 4, (kb != 0 || k != 0) ? 1u : 0u);
                     }
                     umma_commit<CG>(empty_bar(stage));
                     if (++stage == STAGES) stage = 0, phase ^= 1u;
@@ -426,10 +417,7 @@ gemm_fp4_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constan
         uint32_t phase = 0, before_phase = 0, set = 0;
         bool ok = true;
         for (int w = first; ok && w < items; w += step) {
-            const int part = w - w / p.splits * p.splits;
-            const int k0 = (int)((int64_t)part * p.num_kb / p.splits);
-            const int k1 = (int)((int64_t)(part + 1) * p.num_kb / p.splits);
-            for (int kb = k0; kb < k1; ++kb) {
+            for (int kb = 0; kb < p.num_kb; ++kb) {
                 ok = wait_fast(sfull_bar(stage), phase, abort_flag, p.status, 0x8E6);
                 if (ok && before >= 0) ok = wait_fast(empty_bar(before), before_phase, abort_flag, p.status, 0x8E7);
                 ok = __all_sync(0xffffffffu, ok);
@@ -479,9 +467,8 @@ gemm_fp4_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constan
         };
         int local = 0;
         for (int w = first; w < items; w += step, ++local) {
-            const int tile = w / p.splits;
             int m0, n0;
-            tile_coords(tile, p, BM * CG, BN, m0, n0);
+            tile_coords(w, p, BM * CG, BN, m0, n0);
             m0 += (int)rank * BM;
             const int c_base = n0 + half * HC;
             const int row0 = m0 + q * 32;
@@ -518,55 +505,6 @@ gemm_fp4_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constan
             const uint32_t t_row =
                 tmem_base + ((uint32_t)(q * 32) << 16) + (acc ? C::ACC1 : 0u) + (uint32_t)(half * HC);
             uint32_t r[32];
-            if (p.splits > 1) {
-                // park this part's sums; the last of the tile's parts adds
-                // them all up in part order
-                const int wr = warp - 2;
-                constexpr int REGION = NCH * 8 * 32;  // float4 per warp
-                float4* mine = reinterpret_cast<float4*>(p.part) + ((int64_t)w * kEpiWarps + wr) * REGION;
-                for (int c = 0; c < NCH; ++c) {
-                    tmem_ld32(t_row + (uint32_t)(c * 32), r);
-                    if (row_ok)
-#pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            __stcg(mine + (c * 8 + e) * 32 + lane,
-                                   make_float4(__uint_as_float(r[4 * e]), __uint_as_float(r[4 * e + 1]),
-                                               __uint_as_float(r[4 * e + 2]), __uint_as_float(r[4 * e + 3])));
-                }
-                if (shares) release_acc(acc);
-                __threadfence();
-                __syncwarp();
-                int before = 0;
-                int* cnt = p.cnt + tile * kEpiWarps + wr;
-                if (lane == 0) before = atomicAdd(cnt, 1);
-                before = __shfl_sync(0xffffffffu, before, 0);
-                if (before + 1 != p.splits) continue;
-                __threadfence();
-                if (lane == 0) *cnt = 0;  // ready for the next launch
-                for (int c = 0; c < NCH; ++c) {
-                    if (row0 >= p.M || c_base + c * 32 >= p.N) break;
-                    float s[32];
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) s[e] = 0.0f;
-                    if (row_ok)
-                        for (int k = 0; k < p.splits; ++k) {
-                            const float4* src = reinterpret_cast<const float4*>(p.part) +
-                                                (((int64_t)tile * p.splits + k) * kEpiWarps + wr) * REGION;
-#pragma unroll
-                            for (int e = 0; e < 8; ++e) {
-                                const float4 v = __ldcg(src + (c * 8 + e) * 32 + lane);
-                                s[4 * e] += v.x;
-                                s[4 * e + 1] += v.y;
-                                s[4 * e + 2] += v.z;
-                                s[4 * e + 3] += v.w;
-                            }
-                        }
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(s[e]);
-                    epi_chunk<OUT>(p, r, c * 32, c_base + c * 32, row0, rx, rw_w, bias_w, stg, lane, &tmap_y);
-                }
-                continue;
-            }
             // shared columns first: the upper half's last chunks of the first
             // accumulator, the lower half's first ones of the second
             const int turn = C::OVERLAP && acc == 0 && half == 1 ? NCH - C::SHARED : 0;
@@ -592,6 +530,258 @@ gemm_fp4_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constan
         else
             asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(C::TMEM_COLS));
     }
+}
+
+// ---------------------------------------------------------------- few tiles
+// One 128 x 128 tile, or one part of its k-loop (the cluster holds the parts), per
+// CTA. MB: rows of X that are loaded (the tensor core reads whatever is in the
+// others; they only reach rows that are not written). Warp 0 loads, warp 1 issues
+// the MMAs, warps 2..5 bring the scales to tensor memory and then the sums from
+// there to shared memory; all six add the parts and write.
+template <int FMT, int MB>
+struct SCfg {
+    static constexpr int CHUNKS = FMT == SQ_NVFP4 ? 4 : 2;
+    static constexpr int STAGES = MB == 32 ? 4 : 3;
+    // (an MMA reads 128 rows from its stage on: at MB = 32 those of later stages
+    // and of the weight's, inside this block's memory)
+    static constexpr uint32_t A_BYTES = MB * BK / 2;
+    static constexpr uint32_t B_BYTES = 128 * BK / 2;
+    static constexpr uint32_t S_BYTES = CHUNKS * kFp4TileBytes;  // of one operand
+    static constexpr uint32_t TX = A_BYTES + B_BYTES;
+    static constexpr uint32_t B_OFF = STAGES * A_BYTES;
+    static constexpr uint32_t S_OFF = B_OFF + STAGES * B_BYTES;
+    static constexpr uint32_t BAR_OFF = S_OFF + STAGES * 2 * S_BYTES;  // full[S], empty[S], sfull[S], sready[S], done
+    static constexpr uint32_t MISC_OFF = BAR_OFF + (4 * STAGES + 1) * 8;
+    static constexpr uint32_t RX_OFF = MISC_OFF + 16;  // 1 / qs_x of the rows
+    static constexpr uint32_t SMEM_ALLOC = RX_OFF + MB * 4 + 1024;
+    static constexpr int LDP = 132;  // floats per row of the sums (in the ring, once it is drained)
+    static_assert(MB * LDP * 4 <= S_OFF && BM * BK / 2 <= STAGES * B_BYTES, "the sums and an MMA's reads fit in the ring");
+    static_assert(2 * (SMEM_ALLOC + 1024) <= 233472, "two CTAs per SM");
+    static constexpr uint32_t SET_COLS = 2 * CHUNKS * 4;
+    static constexpr uint32_t SF_COL = 128, TMEM_COLS = 256;
+    static_assert(SF_COL + 2 * SET_COLS <= TMEM_COLS, "tensor memory");
+    static constexpr uint32_t idesc(int sf) { return Cfg<FMT, 128, 1>::idesc(sf); }
+};
+constexpr int kSplitThreads = 6 * 32;
+
+template <int FMT, int MB, int OUT>
+__global__ void __launch_bounds__(kSplitThreads, 2)
+gemm_fp4_split_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ CUtensorMap tmap_b,
+                      const __grid_constant__ CUtensorMap tmap_sa, const __grid_constant__ CUtensorMap tmap_sb,
+                      const Params p, const int splits) {
+    using C = SCfg<FMT, MB>;
+    constexpr int STAGES = C::STAGES;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t sbase = smem_u32(smem);
+    const uint32_t bar0 = sbase + C::BAR_OFF;
+    auto full_bar = [&](int s) { return bar0 + 8u * s; };
+    auto empty_bar = [&](int s) { return bar0 + 8u * (STAGES + s); };
+    auto sfull_bar = [&](int s) { return bar0 + 8u * (2 * STAGES + s); };
+    auto sready_bar = [&](int s) { return bar0 + 8u * (3 * STAGES + s); };
+    const uint32_t done_bar = bar0 + 8u * (4 * STAGES);
+    uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + C::MISC_OFF);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::MISC_OFF + 4);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < STAGES; ++s) {
+            mbar_init(full_bar(s), 1);
+            mbar_init(empty_bar(s), 1);
+            mbar_init(sfull_bar(s), 1);
+            mbar_init(sready_bar(s), 4);
+        }
+        mbar_init(done_bar, 1);
+        *abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_holder)),
+                     "r"(C::TMEM_COLS));
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_holder;
+    const int part = blockIdx.x % splits, tile = blockIdx.x / splits;
+    const int nb = tile / p.num_m;
+    const int m0 = (tile - nb * p.num_m) * BM, n0 = nb * 128;
+    const int k0 = (int)((int64_t)part * p.num_kb / splits);
+    const int k1 = (int)((int64_t)(part + 1) * p.num_kb / splits);
+    const int rows = min(p.M - m0, MB);
+    pdl_wait();
+    pdl_trigger();
+    // the scales and biases of the outputs this thread writes, fetched while the
+    // k-loop runs: columns 4 l .. 4 l + 3 (lane l), or l, l + 32, .. where rows do
+    // not start on 16-byte boundaries (a warp's stores then stay together)
+    const int c0 = p.vec_store ? 4 * lane : lane, cs = p.vec_store ? 1 : 32;
+    float rw[4], bias[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const int col = min(n0 + c0 + cs * e, p.N - 1);
+        rw[e] = p.qs_w ? p.qs_w[p.w_per_channel ? col : 0] : 1.0f;
+        bias[e] = p.bias ? p.bias[col] : 0.0f;
+    }
+    float* const rx_s = reinterpret_cast<float*>(smem + C::RX_OFF);
+    if ((int)threadIdx.x < rows)
+        rx_s[threadIdx.x] = p.qs_x ? __frcp_rn(p.qs_x[p.x_per_token ? m0 + (int)threadIdx.x : 0]) : 1.0f;
+    if (warp == 0) {
+        if (lane == 0) {
+            int stage = 0, kb = k0;
+            uint32_t phase = 0;
+            for (; kb < k1; ++kb) {
+                if (!wait_fast(empty_bar(stage), phase ^ 1u, abort_flag, p.status, 0x8F1)) break;
+                mbar_expect_tx(full_bar(stage), C::TX);
+                mbar_expect_tx(sfull_bar(stage), 2 * C::S_BYTES);
+                tma_load_3d<1>(sbase + C::B_OFF + stage * C::B_BYTES, &tmap_b, full_bar(stage), kb * (BK / 2), n0, 0);
+                tma_load_3d<1>(sbase + stage * C::A_BYTES, &tmap_a, full_bar(stage), kb * (BK / 2), m0, 0);
+                const uint32_t sf = sbase + C::S_OFF + stage * 2 * C::S_BYTES;
+                tma_load_3d<1>(sf, &tmap_sb, sfull_bar(stage), kb * (int)(C::S_BYTES / 8), n0 / 128, 0);
+                tma_load_3d<1>(sf + C::S_BYTES, &tmap_sa, sfull_bar(stage), kb * (int)(C::S_BYTES / 8), m0 / 128, 0);
+                if (++stage == STAGES) stage = 0, phase ^= 1u;
+            }
+            // after an abort: the copies that are in flight land before the block leaves
+            if (kb < k1)
+                for (int i = max(k0, kb - STAGES); i < kb; ++i) {
+                    wait_drain(full_bar((i - k0) % STAGES), (uint32_t)((i - k0) / STAGES) & 1u);
+                    wait_drain(sfull_bar((i - k0) % STAGES), (uint32_t)((i - k0) / STAGES) & 1u);
+                }
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            int stage = 0;
+            uint32_t phase = 0, set = 0;
+            for (int kb = k0; kb < k1; ++kb) {
+                if (!wait_fast(full_bar(stage), phase, abort_flag, p.status, 0x8F2) ||
+                    !wait_fast(sready_bar(stage), phase, abort_flag, p.status, 0x8F3))
+                    break;
+                tc_fence_after();
+                const uint32_t a_addr = sbase + stage * C::A_BYTES, b_addr = sbase + C::B_OFF + stage * C::B_BYTES;
+                const uint32_t sfb = tmem + C::SF_COL + set * C::SET_COLS, sfa = sfb + C::CHUNKS * 4;
+                set ^= 1u;
+                const int steps = min(BK / UMMA_K, (p.K - kb * BK + UMMA_K - 1) / UMMA_K);
+#pragma unroll
+                for (int k = 0; k < BK / UMMA_K; ++k) {
+                    if (k >= steps) break;
+                    const int c = FMT == SQ_NVFP4 ? k : k >> 1;
+                    const int sf = FMT == SQ_NVFP4 ? 0 : (k & 1) * 2;
+                    umma_fp4<FMT, 1>(tmem, sdesc(a_addr + k * (UMMA_K / 2)), sdesc(b_addr + k * (UMMA_K / 2)), C::idesc(sf),
+                                     sfa + c * 4, sfb + c * 4, (kb != k0 || k != 0) ? 1u : 0u);
+                }
+                umma_commit<1>(empty_bar(stage));
+                if (++stage == STAGES) stage = 0, phase ^= 1u;
+            }
+            umma_commit<1>(done_bar);
+            wait_drain(done_bar, 0);  // (no MMA is in flight when tensor memory is freed)
+        }
+    } else {
+        const uint32_t quarter = (uint32_t)((warp & 3) * 32) << 16;
+        int stage = 0, before = -2;
+        uint32_t phase = 0, before_phase = 0, set = 0;
+        bool ok = true;
+        for (int kb = k0; kb < k1; ++kb) {
+            ok = wait_fast(sfull_bar(stage), phase, abort_flag, p.status, 0x8F4);
+            if (ok && before >= 0) ok = wait_fast(empty_bar(before), before_phase, abort_flag, p.status, 0x8F5);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            tc_fence_after();
+            uint32_t r[C::SET_COLS];
+            const uint4* sf = reinterpret_cast<const uint4*>(smem + C::S_OFF + stage * 2 * C::S_BYTES) + lane;
+#pragma unroll
+            for (int c = 0; c < 2 * C::CHUNKS; ++c) *reinterpret_cast<uint4*>(r + 4 * c) = sf[c * 32];
+            const uint32_t to = tmem + quarter + C::SF_COL + set * C::SET_COLS;
+#pragma unroll
+            for (uint32_t i = 0; i < C::SET_COLS; i += 16) tmem_st<16>(to + i, r + i);
+            asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(sready_bar(stage));
+            set ^= 1u;
+            if (++before == STAGES) before = 0, before_phase ^= 1u;
+            if (++stage == STAGES) stage = 0, phase ^= 1u;
+        }
+        if (ok) ok = wait_fast(done_bar, 0, abort_flag, p.status, 0x8F6);
+        ok = __all_sync(0xffffffffu, ok);
+        tc_fence_after();
+        // this warp's 32 rows to shared memory, over the drained ring
+        const int row = (warp & 3) * 32 + lane;
+        if (ok && (warp & 3) * 32 < rows) {
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+                uint32_t r[32];
+                tmem_ld32(tmem + quarter + c * 32, r);
+                if (row < rows) {
+                    uint4* to = reinterpret_cast<uint4*>(smem + (row * C::LDP + c * 32) * 4);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) to[e] = make_uint4(r[4 * e], r[4 * e + 1], r[4 * e + 2], r[4 * e + 3]);
+                }
+            }
+        }
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if (splits > 1) cluster_sync_all();  // every part's sums are in its shared memory
+    if (warp == 1) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::TMEM_COLS));
+    }
+    // this part's share of the rows, a warp each
+#pragma unroll
+    for (int e = 0; e < 4; ++e) rw[e] = __frcp_rn(rw[e]);
+    const int r1 = (int)((int64_t)(part + 1) * rows / splits);
+#pragma unroll 2
+    for (int row = (int)((int64_t)part * rows / splits) + warp; row < r1; row += kSplitThreads / 32) {
+        const uint32_t at = sbase + (uint32_t)(row * C::LDP + c0) * 4;
+        float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        for (int s = 0; s < splits; ++s) {
+            float v[4];
+            // (a lone CTA is rank 0 of a cluster of one)
+            const uint32_t from = map_to_rank(at, (uint32_t)s);
+            if (p.vec_store) {
+                asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
+                             : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3])
+                             : "r"(from)
+                             : "memory");
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v[e]) : "r"(from + 128u * e) : "memory");
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[e] += v[e];
+        }
+        const float rx = rx_s[row];
+        float y[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            y[e] = __fmul_rn(acc[e], __fmul_rn(rx, rw[e]));
+            if (p.bias) y[e] = __fadd_rn(y[e], bias[e]);
+        }
+        constexpr int EB = OUT == kOutF32 ? 4 : 2;
+        uint8_t* out = static_cast<uint8_t*>(p.Y) + (((int64_t)m0 + row) * p.ldy + n0 + c0) * EB;
+        uint32_t w[4];
+        if constexpr (OUT == kOutF32) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) w[e] = __float_as_uint(y[e]);
+        } else {
+            w[0] = pack2<OUT>(y[0], y[1]), w[1] = pack2<OUT>(y[2], y[3]);
+        }
+        if (p.vec_store && n0 + c0 + 4 <= p.N) {
+            if constexpr (OUT == kOutF32) *reinterpret_cast<uint4*>(out) = make_uint4(w[0], w[1], w[2], w[3]);
+            else *reinterpret_cast<uint2*>(out) = make_uint2(w[0], w[1]);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (n0 + c0 + cs * e < p.N) {
+                    if constexpr (OUT == kOutF32) *reinterpret_cast<uint32_t*>(out + 4 * cs * e) = w[e];
+                    else *reinterpret_cast<uint16_t*>(out + 2 * cs * e) = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
+                }
+        }
+    }
+    if (splits > 1) cluster_sync_all();  // nobody leaves while its sums are read
 }
 
 // ---------------------------------------------------------------- host side
@@ -622,40 +812,35 @@ bool make_map_scales(CUtensorMap* m, const uint8_t* base, int64_t groups, int64_
 }
 
 struct Plan {
-    int bn = 128, cg = 1, tiles = 0, splits = 1, grid = 0;
-    size_t part_bytes = 0;
+    bool pairs = false;
+    int tiles = 0, splits = 1, grid = 0;
 };
-
-// Counters at a fixed place for every shape: one per warp region of a split's
-// tiles, of which there are fewer than SMs.
-constexpr int kMaxSplitTiles = 256;
-constexpr size_t kCntBytes = (size_t)kMaxSplitTiles * kEpiWarps * sizeof(int);
-static_assert(kCntBytes % 256 == 0, "the parked sums start 256-byte aligned");
 
 Plan plan_fp4(int64_t M, int64_t N, int64_t K) {
     Plan pl;
     const int sms = num_sms();
     const int64_t kb = (K + BK - 1) / BK;
     const int64_t ptiles = ((M + 255) / 256) * ((N + 255) / 256);
-    if (2 * ptiles >= sms) {
-        pl.bn = 256;
-        pl.cg = 2;
+    const int64_t tiles = ((M + 127) / 128) * ((N + 127) / 128);
+    // Pairs above 128 rows and 64 tiles. Measured on B200 (us, one tile or part
+    // per CTA / pairs): 16 x 16384 x 4096 9.4 / 12.6, 1 x 28672 x 7168 23 / 40,
+    // 128 x 4096 x 4096 8.6 / 11.9, 256 x 4096 x 4096 (64 tiles) 11.1 / 11.9,
+    // 512 x 4096 x 4096 (128 tiles) 13.1 / 12.1, 256 x 12288 x 4096 (192) 17.1 / 12.6.
+    if (M > 128 && tiles > 64) {
+        pl.pairs = true;
         pl.tiles = (int)ptiles;
         const int64_t pairs = sms / 2;
         pl.grid = (int)(2 * (ptiles < pairs ? ptiles : pairs));
         return pl;
     }
-    const int64_t tiles = ((M + 127) / 128) * ((N + 127) / 128);
     pl.tiles = (int)tiles;
-    // equal parts of the k-loop, at least two stages each, while all fit at once
-    int64_t s = sms / tiles;
-    if (s > kb / 2) s = kb / 2;
-    if (s > 16) s = 16;
-    if (s > 1 && tiles <= kMaxSplitTiles) {
-        pl.splits = (int)s;
-        pl.part_bytes = kCntBytes + (size_t)(tiles * s) * BM * 128 * sizeof(float);
-    }
-    pl.grid = (int)(tiles * pl.splits < sms ? tiles * pl.splits : sms);
+    // The k-loop in two or four parts while all of them fit at once (two CTAs per
+    // SM), in eight while they leave every CTA an SM of its own; two stages or
+    // more each. 16 x 4096 x 4096 (32 tiles): 10.1 us whole, 8.0 in two parts,
+    // 6.2 in four, 6.7 in eight; 16 x 12288 x 4096 (96 tiles): 10.4, 9.5, 13.4.
+    for (int s = 2; s <= 8; s *= 2)
+        if (tiles * s <= (s == 8 ? sms : 2 * sms) && kb >= 2 * s) pl.splits = s;
+    pl.grid = (int)tiles * pl.splits;
     return pl;
 }
 
@@ -665,8 +850,13 @@ struct Call {
     sq_dtype_t out_dt;
 };
 
-template <int FMT, int BN, int CG, int OUT>
-sq_status_t launch(const char* name, const Call& c, const Plan& pl, Params& p, cudaStream_t stream) {
+sq_status_t map_failed(const char* name) {
+    return set_error(SQ_ERR_CUDA, "%s: cuTensorMapEncodeTiled failed", name);
+}
+
+template <int FMT, int OUT>
+sq_status_t launch_pairs(const char* name, const Call& c, const Plan& pl, Params& p, cudaStream_t stream) {
+    constexpr int BN = 256, CG = 2;
     using C = Cfg<FMT, BN, CG>;
     const int64_t tk = fp4_tiles_k(FMT, c.K);
     CUtensorMap ta, tb, tsa, tsb, ty;
@@ -674,12 +864,11 @@ sq_status_t launch(const char* name, const Call& c, const Plan& pl, Params& p, c
     if (!make_map_codes(&ta, c.Xq, c.M, c.K, BM) || !make_map_codes(&tb, c.Wq, c.N, c.K, BN / CG) ||
         !make_map_scales(&tsa, c.Xs, fp4_tiles_m(c.M), tk, C::CHUNKS, 1) ||
         !make_map_scales(&tsb, c.Ws, fp4_tiles_m(c.N), tk, C::CHUNKS, C::NG))
-        return set_error(SQ_ERR_CUDA, "%s: cuTensorMapEncodeTiled failed", name);
+        return map_failed(name);
     if (OUT != kOutF32 && p.vec_store)
         p.tma_store = make_map_y(&ty, p.Y, c.M, c.N, p.ldy, 1, c.M * p.ldy, OUT == kOutBF16) ? 1 : 0;
     p.num_m = (int)((c.M + BM * CG - 1) / (BM * CG));
     p.num_n = (int)((c.N + BN - 1) / BN);
-    p.num_kb = (int)((c.K + BK - 1) / BK);
     // rows of X per raster group within about 48 MB of L2
     const int64_t per = (int64_t)BM * CG * c.K / 2;
     const int64_t g = (48ll << 20) / per;
@@ -687,17 +876,36 @@ sq_status_t launch(const char* name, const Call& c, const Plan& pl, Params& p, c
     auto fn = gemm_fp4_kernel<FMT, BN, CG, OUT>;
     if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM_ALLOC) != cudaSuccess)
         return check_launch(name);
-    if constexpr (CG == 2)
-        launch_pdl_cluster(fn, dim3(pl.grid), dim3(kThreads), C::SMEM_ALLOC, stream, 2, ta, tb, tsa, tsb, ty, p);
+    launch_pdl_cluster(fn, dim3(pl.grid), dim3(kThreads), C::SMEM_ALLOC, stream, 2, ta, tb, tsa, tsb, ty, p);
+    return check_launch(name);
+}
+
+template <int FMT, int MB, int OUT>
+sq_status_t launch_split(const char* name, const Call& c, const Plan& pl, Params& p, cudaStream_t stream) {
+    using C = SCfg<FMT, MB>;
+    const int64_t tk = fp4_tiles_k(FMT, c.K);
+    CUtensorMap ta, tb, tsa, tsb;
+    if (!make_map_codes(&ta, c.Xq, c.M, c.K, MB) || !make_map_codes(&tb, c.Wq, c.N, c.K, 128) ||
+        !make_map_scales(&tsa, c.Xs, fp4_tiles_m(c.M), tk, C::CHUNKS, 1) ||
+        !make_map_scales(&tsb, c.Ws, fp4_tiles_m(c.N), tk, C::CHUNKS, 1))
+        return map_failed(name);
+    p.num_m = (int)((c.M + BM - 1) / BM);
+    auto fn = gemm_fp4_split_kernel<FMT, MB, OUT>;
+    if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM_ALLOC) != cudaSuccess)
+        return check_launch(name);
+    if (pl.splits > 1)
+        launch_pdl_cluster(fn, dim3(pl.grid), dim3(kSplitThreads), C::SMEM_ALLOC, stream, pl.splits, ta, tb, tsa, tsb, p,
+                           pl.splits);
     else
-        launch_pdl(fn, dim3(pl.grid), dim3(kThreads), C::SMEM_ALLOC, stream, ta, tb, tsa, tsb, ty, p);
+        launch_pdl(fn, dim3(pl.grid), dim3(kSplitThreads), C::SMEM_ALLOC, stream, ta, tb, tsa, tsb, p, 1);
     return check_launch(name);
 }
 
 template <int FMT, int OUT>
 sq_status_t launch_plan(const char* name, const Call& c, const Plan& pl, Params& p, cudaStream_t stream) {
-    if (pl.cg == 2) return launch<FMT, 256, 2, OUT>(name, c, pl, p, stream);
-    return launch<FMT, 128, 1, OUT>(name, c, pl, p, stream);
+    if (pl.pairs) return launch_pairs<FMT, OUT>(name, c, pl, p, stream);
+    if (c.M <= 32) return launch_split<FMT, 32, OUT>(name, c, pl, p, stream);
+    return launch_split<FMT, 128, OUT>(name, c, pl, p, stream);
 }
 
 template <int FMT>
@@ -710,8 +918,8 @@ sq_status_t launch_out(const char* name, const Call& c, const Plan& pl, Params& 
 }  // namespace
 
 size_t gemm_fp4_workspace_bytes(int64_t M, int64_t N, int64_t K) {
-    if (M <= 0 || N <= 0 || K <= 0) return kStatusBytes;
-    return kStatusBytes + plan_fp4(M, N, K).part_bytes;
+    (void)M, (void)N, (void)K;
+    return kStatusBytes;  // the status word of the bounded waits
 }
 
 }  // namespace sq
@@ -735,20 +943,15 @@ extern "C" sq_status_t sq_gemm_fp4(const uint8_t* Xq, const uint8_t* Xs, const u
                "%s: codes and block scales must be 16-byte aligned", name);
     SQ_REQUIRE(workspace && ws_bytes >= sq::kStatusBytes, SQ_ERR_INVALID_ARG, "%s: needs a workspace of %zu bytes", name,
                sq::kStatusBytes);
-    sq::Plan pl = sq::plan_fp4(M, N, K);
-    if (pl.splits > 1 && ws_bytes < sq::kStatusBytes + pl.part_bytes) {
-        // a workspace without room for the parts runs every k-loop whole
-        pl.splits = 1;
-        pl.grid = pl.tiles < sq::num_sms() ? pl.tiles : sq::num_sms();
-    }
+    const sq::Plan pl = sq::plan_fp4(M, N, K);
     const int eb = sq::dtype_bytes(out_dt);
     sq::Params p;
     memset(&p, 0, sizeof(p));
     p.M = (int)M;
     p.N = (int)N;
     p.K = (int)K;
+    p.num_kb = (int)((K + sq::BK - 1) / sq::BK);
     p.tiles = pl.tiles;
-    p.splits = pl.splits;
     p.vec_store = sq::aligned16(Y) && (ldy * eb) % 16 == 0;
     p.qs_x = qs_x;
     p.qs_w = qs_w;
@@ -758,10 +961,6 @@ extern "C" sq_status_t sq_gemm_fp4(const uint8_t* Xq, const uint8_t* Xs, const u
     p.Y = Y;
     p.ldy = ldy;
     p.status = static_cast<int*>(workspace);
-    uint8_t* after = static_cast<uint8_t*>(workspace) + sq::kStatusBytes;
-    p.cnt = reinterpret_cast<int*>(after);
-    p.part = reinterpret_cast<float*>(after + sq::kCntBytes);
-    p.cnt_bytes = (int)sq::kCntBytes;
     const sq::Call c = {Xq, Xs, Wq, Ws, M, N, K, out_dt};
     cudaStream_t s = sq::as_cuda(stream);
     return fmt == SQ_NVFP4 ? sq::launch_out<SQ_NVFP4>(name, c, pl, p, s) : sq::launch_out<SQ_MXFP4>(name, c, pl, p, s);
