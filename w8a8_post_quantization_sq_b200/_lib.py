@@ -482,58 +482,110 @@ def fp4_buffers(rows, K, fmt, device=None):
             torch.empty(rows, dtype=torch.float32, device=dev) if fmt == SQ_NVFP4 else None)
 
 
+# The functions from here on check every tensor once, in one place each: a call
+# of theirs may take the GPU less time than a dozen small Python calls.
+def _current():
+    """The current device (-2 where there is none: no tensor is on it)."""
+    try:
+        return _device()
+    except RuntimeError:
+        return -2
+
+
+def _at(t, device):
+    """Address of a tensor on the current device (None: 0)."""
+    if t is None:
+        return None
+    if t.get_device() != device:
+        raise ValueError(f"tensor on {t.device}, but the current device is cuda:{device}" if t.is_cuda
+                         else "tensor must be on a CUDA device")
+    return t.data_ptr()
+
+
+def _f32(t, device, n, what):
+    """Address of a contiguous fp32 vector of n elements (None: 0)."""
+    if t is None:
+        return None
+    if t.dtype is not torch.float32 or t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous {torch.float32} tensor of {n} elements")
+    return _at(t, device)
+
+
+def _qs(t, device, n, what):
+    """Address of one scale or n of them (None: 0), and whether there are n."""
+    if t is None:
+        return None, 0
+    many = t.numel()
+    if t.dtype is not torch.float32 or not t.is_contiguous() or (many != 1 and many < n):
+        raise ValueError(f"{what} must be a contiguous {torch.float32} tensor that holds 1 or at least {n} scales")
+    return _at(t, device), int(many > 1)
+
+
 def _fp4(codes, scales, fmt, rows, K, what):
     if fmt not in (SQ_NVFP4, SQ_MXFP4):
         raise ValueError(f"unknown format {fmt}")
-    if codes.dtype != torch.uint8 or not codes.is_contiguous() or codes.shape != (rows, K // 2):
+    if codes.dtype is not torch.uint8 or not codes.is_contiguous() or codes.shape != (rows, K // 2):
         raise ValueError(f"{what}: codes must be contiguous uint8 [{rows}, {K // 2}]")
     span = 64 if fmt == SQ_NVFP4 else 128  # elements per tile of four blocks
     need = (rows + 127) // 128 * ((K + span - 1) // span) * 512
-    if scales.dtype != torch.uint8 or not scales.is_contiguous() or scales.numel() < need:
+    if scales.dtype is not torch.uint8 or not scales.is_contiguous() or scales.numel() < need:
         raise ValueError(f"{what}: block scales must be contiguous uint8 of at least {need} bytes")
 
 
+def _rows(t, what):
+    """Shape and row stride of a 2-D tensor with unit inner stride (a single row's stride says nothing)."""
+    rows, cols = t.shape
+    ld, inner = t.stride()
+    if inner != 1 and cols > 1:
+        raise ValueError(f"{what} must be 2-D with unit inner stride")
+    return rows, cols, ld if rows > 1 else cols
+
+
 def sq_quantize_weight_fp4(W, s, fmt, Wq, Ws, qs_w, stream=None):
-    N, K = W.shape
-    _need(W.is_contiguous(), "W must be contiguous")
+    d = _current()
+    N, K, _ = _rows(W, "W")
+    if not W.is_contiguous():
+        raise ValueError("W must be contiguous")
     _fp4(Wq, Ws, fmt, N, K, "Wq, Ws")
     _check("sq_quantize_weight_fp4", lib().sq_quantize_weight_fp4(
-        _ptr(W), _dt(W), N, K, _vec(s, torch.float32, K), int(fmt), _ptr(Wq), _ptr(Ws), _vec(qs_w, torch.float32, N),
-        _stream(stream)))
+        _at(W, d), _DT[W.dtype], N, K, _f32(s, d, K, "s"), fmt, _at(Wq, d), _at(Ws, d), _f32(qs_w, d, N, "qs_w"),
+        stream.cuda_stream if stream is not None else _raw_stream(d)))
 
 
 def sq_quantize_act_fp4(X, s, fmt, per_token, static_qs, Xq, Xs, qs_x, stream=None):
-    M, K = X.shape
+    d = _current()
+    M, K, ld = _rows(X, "X")
     _fp4(Xq, Xs, fmt, M, K, "Xq, Xs")
     _check("sq_quantize_act_fp4", lib().sq_quantize_act_fp4(
-        _ptr(X), _dt(X), M, K, _ld(X), _vec(s, torch.float32, K), int(fmt), int(per_token),
-        _vec(static_qs, torch.float32, 1), _ptr(Xq), _ptr(Xs), _vec(qs_x, torch.float32, M if per_token else 1),
-        _stream(stream)))
+        _at(X, d), _DT[X.dtype], M, K, ld, _f32(s, d, K, "s"), fmt, per_token, _f32(static_qs, d, 1, "static_qs"),
+        _at(Xq, d), _at(Xs, d), _f32(qs_x, d, M if per_token else 1, "qs_x"),
+        stream.cuda_stream if stream is not None else _raw_stream(d)))
 
 
 def sq_dequantize_fp4(Xq, Xs, fmt, qs, Y, stream=None):
     """qs: [M], [1] or None."""
-    M, K = Y.shape
+    d = _current()
+    M, K, ld = _rows(Y, "Y")
     _fp4(Xq, Xs, fmt, M, K, "Xq, Xs")
-    _scales(qs, M, "qs")
+    q, per_row = _qs(qs, d, M, "qs")
     _check("sq_dequantize_fp4", lib().sq_dequantize_fp4(
-        _ptr(Xq), _ptr(Xs), int(fmt), M, K, _vec(qs, torch.float32), int(qs is not None and qs.numel() > 1), _dt(Y),
-        _ptr(Y), _ld(Y), _stream(stream)))
+        _at(Xq, d), _at(Xs, d), fmt, M, K, q, per_row, _DT[Y.dtype], _at(Y, d), ld,
+        stream.cuda_stream if stream is not None else _raw_stream(d)))
 
 
 def sq_gemm_fp4(Xq, Xs, Wq, Ws, fmt, qs_x, qs_w, bias, Y, ws, stream=None):
     """qs_x: [M], [1] or None; qs_w: [N], [1] or None."""
-    M, N = Y.shape
+    d = _current()
+    M, N, ld = _rows(Y, "Y")
     K = Xq.shape[1] * 2
     _fp4(Xq, Xs, fmt, M, K, "Xq, Xs")
     _fp4(Wq, Ws, fmt, N, K, "Wq, Ws")
-    _scales(qs_x, M, "qs_x")
-    _scales(qs_w, N, "qs_w")
+    qx, x_per_token = _qs(qs_x, d, M, "qs_x")
+    qw, w_per_channel = _qs(qs_w, d, N, "qs_w")
     _check("sq_gemm_fp4", lib().sq_gemm_fp4(
-        _ptr(Xq), _ptr(Xs), _ptr(Wq), _ptr(Ws), int(fmt), M, N, K, _vec(qs_x, torch.float32),
-        int(qs_x is not None and qs_x.numel() > 1), _vec(qs_w, torch.float32),
-        int(qs_w is not None and qs_w.numel() > 1), _vec(bias, torch.float32, N), _dt(Y), _ptr(Y), _ld(Y), _ptr(ws),
-        ws.numel(), _stream(stream)))
+        _at(Xq, d), _at(Xs, d), _at(Wq, d), _at(Ws, d), fmt, M, N, K, qx, x_per_token, qw, w_per_channel,
+        _f32(bias, d, N, "bias"), _DT[Y.dtype], _at(Y, d), ld, _at(ws, d), ws.numel(),
+        stream.cuda_stream if stream is not None else _raw_stream(d)))
 
 
 # ---------------------------------------------------------------- attention over a paged int8 cache
@@ -544,49 +596,66 @@ def kv8_cache(num_blocks, heads, block, D, device=None):
     return (*codes, *(torch.ones((num_blocks, heads), dtype=torch.float32, device=dev) for _ in range(2)))
 
 
-def _kv8(Kc, Vc, kqs, vqs, cu_q, seq_lens, block_table):
-    if (Kc.dtype != torch.int8 or Vc.dtype != torch.int8 or Kc.dim() != 4 or Kc.shape != Vc.shape or
+def _kv8(Kc, Vc, kqs, vqs, cu_q, seq_lens, block_table, d):
+    """The cache's and the batch's addresses and sizes."""
+    shape = Kc.shape
+    if (Kc.dtype is not torch.int8 or Vc.dtype is not torch.int8 or len(shape) != 4 or Vc.shape != shape or
             not Kc.is_contiguous() or not Vc.is_contiguous()):
         raise ValueError("Kc and Vc must be contiguous int8 [num_blocks, Hkv, block, D]")
-    if kqs.shape != Kc.shape[:2] or vqs.shape != Kc.shape[:2]:
+    num_blocks, heads, block, D = shape
+    if kqs.shape != shape[:2] or vqs.shape != shape[:2]:
         raise ValueError("kqs and vqs must be [num_blocks, Hkv]")
     B = seq_lens.numel()
-    if (block_table.dim() != 2 or block_table.dtype != torch.int32 or block_table.shape[0] != B or
-            block_table.stride(1) != 1 and block_table.shape[1] > 1):
+    if seq_lens.dtype is not torch.int32 or not seq_lens.is_contiguous():
+        raise ValueError("seq_lens must be contiguous int32")
+    if cu_q.dtype is not torch.int32 or cu_q.numel() != B + 1 or not cu_q.is_contiguous():
+        raise ValueError(f"cu_q must be a contiguous int32 tensor of {B + 1} elements")
+    if block_table.dtype is not torch.int32 or block_table.dim() != 2 or block_table.shape[0] != B:
         raise ValueError(f"block_table must be int32 [{B}, max_blocks] with unit inner stride")
-    return (_vec(kqs, torch.float32), _vec(vqs, torch.float32), _vec(cu_q, torch.int32, B + 1),
-            _vec(seq_lens, torch.int32), B, _ptr(block_table), block_table.shape[1],
-            max(block_table.stride(0), block_table.shape[1]) if B < 2 else block_table.stride(0))
+    _, max_blocks, ldb = _rows(block_table, "block_table")
+    n = num_blocks * heads
+    return ((_at(Kc, d), _at(Vc, d)), (_f32(kqs, d, n, "kqs"), _f32(vqs, d, n, "vqs")),
+            (_at(cu_q, d), _at(seq_lens, d), B, _at(block_table, d), max_blocks, ldb), num_blocks, heads, block, D)
 
 
 def _heads(t, what):
-    """Token stride of [T, heads, D] whose heads lie back to back (a single token's stride says nothing)."""
+    """Shape and token stride of [T, heads, D] whose heads lie back to back (a single token's stride says nothing)."""
+    if t.dim() != 3:
+        raise ValueError(f"{what} must be [T, heads, D]")
     T, heads, D = t.shape
-    if t.stride(2) != 1 or heads > 1 and t.stride(1) != D:
+    ld, head, inner = t.stride()
+    if inner != 1 or heads > 1 and head != D:
         raise ValueError(f"{what} must be [T, heads, D] with each token's heads back to back")
-    return t.stride(0) if T > 1 else heads * D
+    return T, heads, D, ld if T > 1 else heads * D
 
 
 def sq_kv8_append(Kn, Vn, cu_q, seq_lens, block_table, Kc, Vc, kqs, vqs, stream=None):
     """Kn, Vn [T, Hkv, D] (token stride free) into the cache; seq_lens counts the new tokens."""
-    ks, vs, cu, lens, B, table, max_blocks, ldb = _kv8(Kc, Vc, kqs, vqs, cu_q, seq_lens, block_table)
-    _need(Kn.dim() == 3 and Vn.shape == Kn.shape and Vn.dtype == Kn.dtype, "Kn and Vn must have one shape and dtype")
-    T, heads, D = Kn.shape
-    num_blocks, cache_heads, block, width = Kc.shape
-    _need(heads == cache_heads and D == width, "Kn and the cache must have the same heads and head width")
+    d = _current()
+    codes, scales, batch, num_blocks, heads, block, D = _kv8(Kc, Vc, kqs, vqs, cu_q, seq_lens, block_table, d)
+    T, h, width, ldk = _heads(Kn, "Kn")
+    Tv, hv, width_v, ldv = _heads(Vn, "Vn")
+    if T != Tv or h != hv or width != width_v or Vn.dtype is not Kn.dtype:
+        raise ValueError("Kn and Vn must have one shape and dtype")
+    if h != heads or width != D:
+        raise ValueError("Kn and the cache must have the same heads and head width")
     _check("sq_kv8_append", lib().sq_kv8_append(
-        _ptr(Kn), _ptr(Vn), _dt(Kn), T, heads, D, _heads(Kn, "Kn"), _heads(Vn, "Vn"), cu, lens, B, table, max_blocks,
-        ldb, _ptr(Kc), _ptr(Vc), ks, vs, num_blocks, block, _stream(stream)))
+        _at(Kn, d), _at(Vn, d), _DT[Kn.dtype], T, heads, D, ldk, ldv, *batch, *codes, *scales, num_blocks, block,
+        stream.cuda_stream if stream is not None else _raw_stream(d)))
 
 
 def sq_kv8_attention(Q, Kc, Vc, kqs, vqs, cu_q, seq_lens, block_table, scale, causal, max_q, Y, ws, stream=None):
     """Q, Y [T, Hq, D] (token strides free); max_q: the largest number of new tokens of a sequence."""
-    ks, vs, cu, lens, B, table, max_blocks, ldb = _kv8(Kc, Vc, kqs, vqs, cu_q, seq_lens, block_table)
-    _need(Q.dim() == 3 and Y.shape == Q.shape and Y.dtype == Q.dtype, "Q and Y must have one shape and dtype")
-    T, hq, D = Q.shape
-    num_blocks, heads, block, width = Kc.shape
-    _need(D == width, "Q and the cache must have the same head width")
+    d = _current()
+    codes, scales, batch, num_blocks, heads, block, D = _kv8(Kc, Vc, kqs, vqs, cu_q, seq_lens, block_table, d)
+    T, hq, width, ldq = _heads(Q, "Q")
+    Ty, hy, width_y, ldy = _heads(Y, "Y")
+    if T != Ty or hq != hy or width != width_y or Y.dtype is not Q.dtype:
+        raise ValueError("Q and Y must have one shape and dtype")
+    if width != D:
+        raise ValueError("Q and the cache must have the same head width")
+    cu, lens, B, table, max_blocks, ldb = batch
     _check("sq_kv8_attention", lib().sq_kv8_attention(
-        _ptr(Q), _dt(Q), T, hq, heads, D, _heads(Q, "Q"), _ptr(Kc), _ptr(Vc), ks, vs, num_blocks, block, cu, lens, B,
-        table, max_blocks, ldb, float(scale), int(causal), int(max_q), _ptr(Y), _heads(Y, "Y"), _ptr(ws), ws.numel(),
-        _stream(stream)))
+        _at(Q, d), _DT[Q.dtype], T, hq, heads, D, ldq, *codes, *scales, num_blocks, block, cu, lens, B, table,
+        max_blocks, ldb, scale, causal, max_q, _at(Y, d), ldy, _at(ws, d), ws.numel(),
+        stream.cuda_stream if stream is not None else _raw_stream(d)))
