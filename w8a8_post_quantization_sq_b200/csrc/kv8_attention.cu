@@ -91,59 +91,85 @@ __device__ __forceinline__ uint32_t movmatrix(uint32_t v) {
     return r;
 }
 
-// A block's range of the list of key tiles, as pieces: the part of the range
-// inside one row tile. Every warp walks the same sequence.
+// floor(a / b); a call, so that the 64-bit division is in the code once.
+static __device__ __noinline__ int64_t div_floor(int64_t a, int b) {
+    return a < (1ll << 31) ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
+}
+
 template <int ROWS>
 __device__ __forceinline__ Seq seq_of(const AttnArgs& a, int b) {
     Seq s = seq_of<ROWS, kTile>(a, b);
     if ((int64_t)s.n * a.G > a.row_limit) s.rt = 0;
     return s;
 }
+
+// A block's range of the list of key tiles, as pieces: the part of the range
+// inside one row tile. Every warp walks the same sequence.
 template <int ROWS>
 struct Walk {
-    int64_t it, end, total, units;
-    int b, item, k0, k1;
+    int64_t it, end, total;
+    int units, b, item, k0, k1;
     bool first;
     Seq s;
-    __device__ __forceinline__ int64_t start_of(int64_t c) const { return c * total / units; }
-    __device__ __forceinline__ int owner_of(int64_t x) const { return (int)(((x + 1) * units + total - 1) / total - 1); }
+    __device__ __forceinline__ int64_t start_of(int c) const { return div_floor(c * total, units); }
+    // the unit whose range holds x: the first c with start_of(c + 1) > x
+    __device__ __forceinline__ int owner_of(int64_t x) const {
+        // (units fits 11 bits, so (x + 1) * units stays inside 64; the quotient
+        // by `total` is below units)
+        const int64_t n = (x + 1) * units + total - 1;
+        if (n < (1ll << 31)) return (int)((uint32_t)n / (uint32_t)total) - 1;
+        return (int)(n / total - 1);
+    }
 
     __device__ __forceinline__ void init(const AttnArgs& a, int lane) {
-        int64_t sum = 0;
-        for (int i = lane; i < a.B; i += 32) sum += seq_of<ROWS>(a, i).work(a.Hkv);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        total = sum;
-        units = min((int64_t)gridDim.x, total);
-        it = end = 0;
-        b = 0;
-        first = true;
-        if (blockIdx.x >= units) return;
-        it = start_of(blockIdx.x);
-        end = start_of(blockIdx.x + 1);
-        // the sequence that holds `it`
-        int64_t before = 0;
-        for (int base = 0; base < a.B; base += 32) {
-            const int64_t w = base + lane < a.B ? seq_of<ROWS>(a, base + lane).work(a.Hkv) : 0;
-            int64_t inc = w;
-#pragma unroll
+        // 32 sequences a look: their work, and the work up to each of them
+        Seq mine;
+        int64_t w, inc;
+        auto look = [&](int base) {
+            mine = seq_of<ROWS>(a, min(base + lane, a.B - 1));
+            w = base + lane < a.B ? mine.work(a.Hkv) : 0;
+            inc = w;
+#pragma unroll 1
             for (int o = 1; o < 32; o <<= 1) {
                 const int64_t up = __shfl_up_sync(0xffffffffu, inc, o);
                 if (lane >= o) inc += up;
             }
-            const unsigned past = __ballot_sync(0xffffffffu, before + inc > it);
-            if (past) {
-                const int l = __ffs(past) - 1;
-                b = base + l;
-                before += __shfl_sync(0xffffffffu, inc - w, l);
-                break;
-            }
+        };
+        total = 0;
+        int base = 0;
+#pragma unroll 1
+        for (; base < a.B; base += 32) {
+            look(base);
+            total += __shfl_sync(0xffffffffu, inc, 31);
+        }
+        units = (int)min((int64_t)gridDim.x, total);
+        it = end = 0;
+        first = true;
+        b = item = k0 = 0;
+        if ((int)blockIdx.x >= units) return;
+        it = start_of(blockIdx.x);
+        end = start_of(blockIdx.x + 1);
+        // the sequence that holds `it` (up to 32 sequences are still at hand)
+        int64_t before = 0;
+        unsigned past;
+        base = 0;
+#pragma unroll 1
+        for (;; base += 32) {
+            if (a.B > 32) look(base);
+            past = __ballot_sync(0xffffffffu, before + inc > it);
+            if (past) break;
             before += __shfl_sync(0xffffffffu, inc, 31);
         }
-        s = seq_of<ROWS>(a, b);
-        const int64_t r = it - before;
-        item = (int)(r / s.tiles);
-        k0 = (int)(r - (int64_t)item * s.tiles);
+        const int l = __ffs(past) - 1;
+        b = base + l;
+        before += __shfl_sync(0xffffffffu, inc - w, l);
+        s.lo = __shfl_sync(0xffffffffu, mine.lo, l);
+        s.n = __shfl_sync(0xffffffffu, mine.n, l);
+        s.len = __shfl_sync(0xffffffffu, mine.len, l);
+        s.rt = __shfl_sync(0xffffffffu, mine.rt, l);
+        s.tiles = __shfl_sync(0xffffffffu, mine.tiles, l);
+        item = (int)div_floor(it - before, s.tiles);
+        k0 = (int)(it - before - (int64_t)item * s.tiles);
     }
     // The next piece: tiles [k0, k1) of row tile `item` of sequence b.
     __device__ __forceinline__ bool next(const AttnArgs& a) {
@@ -470,19 +496,6 @@ kv8_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
         float M = -INFINITY, L = 0.0f, acc[CPT];
 #pragma unroll
         for (int e = 0; e < CPT; ++e) acc[e] = 0.0f;
-        // adds another part of the keys (m, l, O) to (M, L, acc); M is final
-        auto add = [&](float mx, float lx, const float* from) {
-            const float f = mx == -INFINITY ? 0.0f : ex2(mx - M);
-            L += mx == -INFINITY ? lx : lx * f;  // (NaN scores leave m at -inf and l NaN)
-#pragma unroll
-            for (int e = 0; e < CPT; e += 4) {
-                const float4 v = __ldcg(reinterpret_cast<const float4*>(from + e));
-                acc[e] = fmaf(v.x, f, acc[e]);
-                acc[e + 1] = fmaf(v.y, f, acc[e + 1]);
-                acc[e + 2] = fmaf(v.z, f, acc[e + 2]);
-                acc[e + 3] = fmaf(v.w, f, acc[e + 3]);
-            }
-        };
 #pragma unroll
         for (int x = 0; x < kCWarps; ++x) M = fmaxf(M, ml[x * ROWS + row]);
 #pragma unroll
@@ -508,38 +521,73 @@ kv8_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
                 __stcg(mine + ROWS * D + row, M);
                 __stcg(mine + ROWS * D + ROWS + row, L);
             }
-            __threadfence();
-            asm volatile("bar.sync 1, 128;" ::: "memory");
             const int64_t i0 = w.it - w.k0;
             const int c_lo = w.owner_of(i0);
+            asm volatile("bar.sync 1, 128;" ::: "memory");
             if (threadIdx.x == 0) {
+                // (the barrier orders the block's stores before this fence, which
+                // makes them visible before the count)
+                __threadfence();
                 const int before = atomicAdd(a.cnt + c_lo, w.k1 - w.k0);
                 const bool is_last = before + (w.k1 - w.k0) == w.s.tiles;
                 if (is_last) a.cnt[c_lo] = 0;  // ready for the next launch
+                __threadfence();
                 *last_flag = is_last;
             }
             asm volatile("bar.sync 1, 128;" ::: "memory");
             write = *last_flag != 0;
             if (write) {
-                __threadfence();
                 const int c_hi = w.owner_of(i0 + w.s.tiles - 1);
                 // the row tile is the last piece of the range it starts in
                 // (unless it starts that range), the first of the later ones
-                const float* p_lo =
-                    a.part + (int64_t)(c_lo * 2 + (w.start_of(c_lo) == i0 ? 0 : 1)) * PART;
-                const float* p_hi = a.part + (int64_t)(c_lo + 1) * 2 * PART;
-                const int more = c_hi - c_lo;
-                M = __ldcg(p_lo + ROWS * D + row);
-#pragma unroll 8
-                for (int x = 0; x < more; ++x) M = fmaxf(M, __ldcg(p_hi + (int64_t)x * 2 * PART + ROWS * D + row));
+                const float* from = a.part + (int64_t)(c_lo * 2 + (w.start_of(c_lo) == i0 ? 0 : 1)) * PART;
+                const int n = c_hi - c_lo + 1;
+                M = -INFINITY;
                 L = 0.0f;
 #pragma unroll
                 for (int e = 0; e < CPT; ++e) acc[e] = 0.0f;
-                add(__ldcg(p_lo + ROWS * D + row), __ldcg(p_lo + ROWS * D + ROWS + row), p_lo + row * D + col);
-#pragma unroll 4
-                for (int x = 0; x < more; ++x) {
-                    const float* p = p_hi + (int64_t)x * 2 * PART;
-                    add(__ldcg(p + ROWS * D + row), __ldcg(p + ROWS * D + ROWS + row), p + row * D + col);
+                // four parts' loads at a time, joined in order
+                constexpr int PB = 4;
+#pragma unroll 1
+                for (int x0 = 0; x0 < n; x0 += PB) {
+                    float mp[PB], lp[PB];
+                    float4 op[PB][CPT / 4];
+#pragma unroll
+                    for (int x = 0; x < PB; ++x) {
+                        mp[x] = -INFINITY;
+                        lp[x] = 0.0f;
+                        if (x0 + x < n) {
+                            const float* p = x0 + x == 0 ? from : a.part + (int64_t)(c_lo + x0 + x) * 2 * PART;
+                            mp[x] = __ldcg(p + ROWS * D + row);
+                            lp[x] = __ldcg(p + ROWS * D + ROWS + row);
+#pragma unroll
+                            for (int e = 0; e < CPT / 4; ++e)
+                                op[x][e] = __ldcg(reinterpret_cast<const float4*>(p + row * D + col) + e);
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < CPT / 4; ++e) op[x][e] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                        }
+                    }
+                    float to = M;
+#pragma unroll
+                    for (int x = 0; x < PB; ++x) to = fmaxf(to, mp[x]);
+                    const float keep = M == -INFINITY ? 0.0f : ex2(M - to);
+                    if (M != -INFINITY) L *= keep;  // (NaN scores leave m at -inf and l NaN)
+                    M = to;
+#pragma unroll
+                    for (int e = 0; e < CPT; ++e) acc[e] *= keep;
+#pragma unroll
+                    for (int x = 0; x < PB; ++x) {
+                        const float f = mp[x] == -INFINITY ? 0.0f : ex2(mp[x] - to);
+                        L += mp[x] == -INFINITY ? lp[x] : lp[x] * f;
+#pragma unroll
+                        for (int e = 0; e < CPT / 4; ++e) {
+                            acc[4 * e] = fmaf(op[x][e].x, f, acc[4 * e]);
+                            acc[4 * e + 1] = fmaf(op[x][e].y, f, acc[4 * e + 1]);
+                            acc[4 * e + 2] = fmaf(op[x][e].z, f, acc[4 * e + 2]);
+                            acc[4 * e + 3] = fmaf(op[x][e].w, f, acc[4 * e + 3]);
+                        }
+                    }
                 }
             }
         }
