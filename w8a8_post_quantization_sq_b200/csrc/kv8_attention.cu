@@ -21,13 +21,13 @@
 // lose bits that the fp32 sum could not hold either).
 //
 // Work: rows (new token, query head of the group) of one sequence and K/V head
-// make row tiles of 8 or 16; the keys of each row tile are cut into tiles of 64,
+// make row tiles of 8 or 16; the keys of each row tile are cut into tiles of 64 (128),
 // and the list of all tiles is cut into one contiguous range per block (the
 // lengths are on the device; every block works out its own range). A row tile
 // whose keys fall into several ranges is joined by the block that finishes last,
 // in range order, so results do not depend on timing.
-// In a block, one warp brings 64 keys' K and V by TMA (swizzled, ring of
-// stages), and four warps take 16 keys each. A decode step has 1 to 16 rows per
+// In a block, one warp brings a tile's K and V by TMA (swizzled, ring of stages),
+// and four warps take 16 (32) keys each. A decode step has 1 to 16 rows per
 // K/V head, an eighth of the smallest tcgen05 tile, and is bound by the cache's
 // bytes and by the conversions, so the products are mma.m16n8k16 with the keys
 // (K) and the columns (V) on the 16-wide side and 8 rows on the other: half the
@@ -42,8 +42,12 @@ namespace sq {
 
 namespace {
 
-constexpr int kTile = 64;     // keys per stage
-constexpr int kSub = 16;      // keys per warp of a stage
+constexpr int kSub = 16;      // keys that one MMA takes
+// 16-key parts per warp and stage: a stage is 16 KB at either head width. (At D =
+// 64 with one part, the per-stage work of a warp, waits, maximum and branches, was
+// as long as the products: 16 sequences x 4 tokens of up to 4000 keys took 25.5 us,
+// with two 21.5.)
+constexpr int parts_of(int d) { return d == 64 ? 2 : 1; }
 constexpr int kCWarps = 4;    // consumer warps
 constexpr int kThreadsA = 32 * (kCWarps + 1);
 constexpr int kStages = 3;
@@ -55,10 +59,13 @@ constexpr int ctas_per_sm(int nr) { return nr == 1 ? 3 : 2; }
 template <int D, int NR>
 struct ACfg {
     static constexpr int ROWS = 8 * NR;
-    static constexpr uint32_t KV = kTile * D;  // bytes of one stage's K (and of its V)
+    static constexpr int PARTS = parts_of(D);
+    static constexpr int TILE = kCWarps * kSub * PARTS;  // keys per stage
+    static constexpr int NPART = TILE / kSub;            // 16-key parts per stage
+    static constexpr uint32_t KV = TILE * D;             // bytes of one stage's K (and of its V)
     static constexpr uint32_t STAGE = 2 * KV;
-    static constexpr uint32_t SC_OFF = kStages * STAGE;              // float4 [stages][4]: 1/kqs, -log2 vqs, vqs
-    static constexpr uint32_t BAR_OFF = SC_OFF + kStages * 4 * 16;   // full[S], empty[S]
+    static constexpr uint32_t SC_OFF = kStages * STAGE;                  // float4 [stages][parts]: 1/kqs, -log2 vqs, vqs
+    static constexpr uint32_t BAR_OFF = SC_OFF + kStages * NPART * 16;   // full[S], empty[S]
     static constexpr uint32_t MISC_OFF = BAR_OFF + 2 * kStages * 8;  // abort flag, last flag
     static constexpr uint32_t ML_OFF = MISC_OFF + 16;                // m, l [warps][rows]
     static constexpr int LDO = D + 4;                                // floats per row of a warp's O
@@ -96,16 +103,16 @@ static __device__ __noinline__ int64_t div_floor(int64_t a, int b) {
     return a < (1ll << 31) ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
 }
 
-template <int ROWS>
-__device__ __forceinline__ Seq seq_of(const AttnArgs& a, int b) {
-    Seq s = seq_of<ROWS, kTile>(a, b);
+template <int ROWS, int KEYS>
+__device__ __forceinline__ Seq short_seq(const AttnArgs& a, int b) {
+    Seq s = seq_of<ROWS, KEYS>(a, b);
     if ((int64_t)s.n * a.G > a.row_limit) s.rt = 0;
     return s;
 }
 
 // A block's range of the list of key tiles, as pieces: the part of the range
 // inside one row tile. Every warp walks the same sequence.
-template <int ROWS>
+template <int ROWS, int KEYS>
 struct Walk {
     int64_t it, end, total;
     int units, b, item, k0, k1;
@@ -126,7 +133,7 @@ struct Walk {
         Seq mine;
         int64_t w, inc;
         auto look = [&](int base) {
-            mine = seq_of<ROWS>(a, min(base + lane, a.B - 1));
+            mine = short_seq<ROWS, KEYS>(a, min(base + lane, a.B - 1));
             w = base + lane < a.B ? mine.work(a.Hkv) : 0;
             inc = w;
 #pragma unroll 1
@@ -175,7 +182,7 @@ struct Walk {
     __device__ __forceinline__ bool next(const AttnArgs& a) {
         if (it >= end) return false;
         while (item >= a.Hkv * s.rt) {
-            s = seq_of<ROWS>(a, ++b);
+            s = short_seq<ROWS, KEYS>(a, ++b);
             item = 0;
         }
         k1 = (int)min((int64_t)s.tiles, k0 + (end - it));
@@ -215,7 +222,7 @@ kv8_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
     __syncthreads();
     pdl_wait();
     pdl_trigger();
-    Walk<ROWS> w;
+    Walk<ROWS, C::TILE> w;
     w.init(a, lane);
     int stage = 0;
     uint32_t phase = 0;
@@ -228,33 +235,34 @@ kv8_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
         for (; ok && w.next(a); w.done()) {
             const int h = w.item / w.s.rt, rt = w.item - h * w.s.rt;
             const int vis = w.seen(a, rt * ROWS + ROWS - 1);
-            const int last = min(w.k1, (vis + kTile - 1) / kTile);
+            const int last = min(w.k1, (vis + C::TILE - 1) / C::TILE);
             const int32_t* row = a.table + (int64_t)w.b * a.ldb;
-            // lane l looks after part l of eight tiles' 32 parts; the next
-            // eight tiles' block numbers are on their way meanwhile
+            // lane l looks after part l of the next few tiles' 32 parts; the block
+            // numbers of those after them are on their way meanwhile
+            constexpr int LOOK = 32 / C::NPART;
             auto block_of = [&](int t0) {
-                const int key = t0 * kTile + lane * kSub;
+                const int key = t0 * C::TILE + lane * kSub;
                 return key < vis ? __ldg(row + (key >> a.block_log2)) : -1;
             };
             int blk_next = block_of(w.k0);
-            for (int t0 = w.k0; ok && t0 < last; t0 += 8) {
-                const int key = t0 * kTile + lane * kSub;
+            for (int t0 = w.k0; ok && t0 < last; t0 += LOOK) {
+                const int key = t0 * C::TILE + lane * kSub;
                 const int64_t blk = blk_next >= 0 && blk_next < a.num_blocks ? blk_next : -1;
                 float kq = __uint_as_float(0x7fffffffu), vq = kq;  // no such block: NaN scales, nothing read
                 if (blk >= 0) {
                     kq = __ldg(a.kqs + blk * a.Hkv + h);
                     vq = __ldg(a.vqs + blk * a.Hkv + h);
                 }
-                if (t0 + 8 < last) blk_next = block_of(t0 + 8);
+                if (t0 + LOOK < last) blk_next = block_of(t0 + LOOK);
                 const int y = h * a.block + (key & (a.block - 1));
-                for (int t = t0; t < min(t0 + 8, last); ++t) {
+                for (int t = t0; t < min(t0 + LOOK, last); ++t) {
                     ok = wait_fast(empty_bar(stage), phase ^ 1u, abort_flag, a.status, 0x7E1);
                     if (!__all_sync(0xffffffffu, ok)) {
                         ok = false;
                         break;
                     }
-                    const int sub = lane - (t - t0) * 4;
-                    const bool mine_now = sub >= 0 && sub < 4;
+                    const int sub = lane - (t - t0) * C::NPART;
+                    const bool mine_now = sub >= 0 && sub < C::NPART;
                     const bool copy = mine_now && blk >= 0 && sub % per_box == 0;
                     const int boxes = __popc(__ballot_sync(0xffffffffu, copy));
                     if (lane == 0) mbar_expect_tx_only(full_bar(stage), (uint32_t)(2 * boxes * a.box * D));
@@ -265,7 +273,7 @@ kv8_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
                         tma_load_3d<1>(dst + C::KV, &map_v, full_bar(stage), 0, y, (int)blk);
                     }
                     // the scales arrive while the copies run
-                    if (mine_now) sc[stage * 4 + sub] = make_float4(__frcp_rn(kq), -__log2f(vq), vq, 0.0f);
+                    if (mine_now) sc[stage * C::NPART + sub] = make_float4(__frcp_rn(kq), -__log2f(vq), vq, 0.0f);
                     __syncwarp();
                     if (lane == 0) mbar_arrive(full_bar(stage));
                     issued |= 1u << stage;
@@ -292,7 +300,7 @@ kv8_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
         const int rows = w.s.n * a.G;  // rows of the sequence
         const int r0 = rt * ROWS;
         const int vis_last = w.seen(a, r0 + ROWS - 1), vis_first = w.seen(a, r0);
-        const int last = min(w.k1, (vis_last + kTile - 1) / kTile);
+        const int last = min(w.k1, (vis_last + C::TILE - 1) / C::TILE);
         // q of row g of each group of 8: lane c holds columns [c D/4, (c + 1)
         // D/4), as the B operand of k-step j the columns 4 j .. 4 j + 3 of those
         // (the same permutation of the summed axis as K's below)
@@ -348,69 +356,65 @@ kv8_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
         for (int t = w.k0; t < last; ++t) {
             if (ok) ok = wait_fast(full_bar(stage), phase, abort_flag, a.status, 0x7E2);
             ok = __all_sync(0xffffffffu, ok);
-            const int key0 = t * kTile + warp * kSub;
+            constexpr int PARTS = C::PARTS;
+            const int key0 = t * C::TILE + warp * (kSub * PARTS);
             if (ok && key0 < vis_last) {
-                const float4 sc = reinterpret_cast<const float4*>(smem + C::SC_OFF)[stage * 4 + warp];
-                const uint32_t kb = sbase + stage * C::STAGE + warp * kSub * D, vb = kb + C::KV;
-                // keys g and g + 8: lane c's D / 4 bytes are one or two 16-byte
-                // units, swizzled by row
-                uint32_t kw[2][D / 16];
+                const float4* scs = reinterpret_cast<const float4*>(smem + C::SC_OFF) + stage * C::NPART + warp * PARTS;
+                const uint32_t kb0 = sbase + stage * C::STAGE + warp * (kSub * PARTS) * D;
+                // scores: keys g (elements 0, 1), g + 8 (2, 3) of each part; rows 2 c, 2 c + 1
+                float s[PARTS][NR][4];
 #pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    const int row = g + 8 * x;
-                    if constexpr (D == 128) {
-                        const uint4 u0 = lds128(kb + row * D + (((2 * c) ^ g) << 4));
-                        const uint4 u1 = lds128(kb + row * D + (((2 * c + 1) ^ g) << 4));
-                        kw[x][0] = u0.x, kw[x][1] = u0.y, kw[x][2] = u0.z, kw[x][3] = u0.w;
-                        kw[x][4] = u1.x, kw[x][5] = u1.y, kw[x][6] = u1.z, kw[x][7] = u1.w;
-                    } else {
-                        const uint4 u0 = lds128(kb + row * D + ((c ^ (g >> 1)) << 4));
-                        kw[x][0] = u0.x, kw[x][1] = u0.y, kw[x][2] = u0.z, kw[x][3] = u0.w;
+                for (int u = 0; u < PARTS; ++u) {
+                    // keys g and g + 8: lane c's D / 4 bytes are one or two 16-byte
+                    // units, swizzled by row
+                    const uint32_t kb = kb0 + u * kSub * D;
+                    uint32_t kw[2][D / 16];
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        const int row = g + 8 * x;
+                        if constexpr (D == 128) {
+                            const uint4 u0 = lds128(kb + row * D + (((2 * c) ^ g) << 4));
+                            const uint4 u1 = lds128(kb + row * D + (((2 * c + 1) ^ g) << 4));
+                            kw[x][0] = u0.x, kw[x][1] = u0.y, kw[x][2] = u0.z, kw[x][3] = u0.w;
+                            kw[x][4] = u1.x, kw[x][5] = u1.y, kw[x][6] = u1.z, kw[x][7] = u1.w;
+                        } else {
+                            const uint4 u0 = lds128(kb + row * D + ((c ^ (g >> 1)) << 4));
+                            kw[x][0] = u0.x, kw[x][1] = u0.y, kw[x][2] = u0.z, kw[x][3] = u0.w;
+                        }
                     }
-                }
-                // V: this lane's keys are 2 c, 2 c + 1, 2 c + 8, 2 c + 9, its
-                // columns [g DG, (g + 1) DG)
-                uint32_t vw[4][D / 32];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int row = 2 * c + (e & 1) + (e >> 1) * 8;
-                    if constexpr (D == 128) {
-                        const uint4 u = lds128(vb + row * D + ((g ^ (row & 7)) << 4));
-                        vw[e][0] = u.x, vw[e][1] = u.y, vw[e][2] = u.z, vw[e][3] = u.w;
-                    } else {
-                        const uint2 u = lds64(vb + row * D + (((g >> 1) ^ ((row >> 1) & 3)) << 4) + (g & 1) * 8);
-                        vw[e][0] = u.x, vw[e][1] = u.y;
+                    for (int z = 0; z < NR; ++z)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) s[u][z][e] = 0.0f;
+#pragma unroll
+                    for (int j = 0; j < NK; ++j) {
+                        const uint32_t u0 = kw[0][j] ^ 0x80808080u, u1 = kw[1][j] ^ 0x80808080u;
+                        const uint32_t af[4] = {half2_of(u0, 0x4140), half2_of(u1, 0x4140), half2_of(u0, 0x4342),
+                                                half2_of(u1, 0x4342)};
+#pragma unroll
+                        for (int z = 0; z < NR; ++z) mma16816(s[u][z], af, qf[z][j][0], qf[z][j][1]);
                     }
-                }
-                float s[NR][4];  // keys g (elements 0, 1), g + 8 (2, 3); rows 2 c, 2 c + 1
-#pragma unroll
-                for (int z = 0; z < NR; ++z)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) s[z][e] = 0.0f;
-#pragma unroll
-                for (int j = 0; j < NK; ++j) {
-                    const uint32_t u0 = kw[0][j] ^ 0x80808080u, u1 = kw[1][j] ^ 0x80808080u;
-                    const uint32_t af[4] = {half2_of(u0, 0x4140), half2_of(u1, 0x4140), half2_of(u0, 0x4342),
-                                            half2_of(u1, 0x4342)};
-#pragma unroll
-                    for (int z = 0; z < NR; ++z) mma16816(s[z], af, qf[z][j][0], qf[z][j][1]);
                 }
                 // scores in log2 with the V scale folded in
-                const bool masked = key0 + kSub > vis_first;
+                const bool masked = key0 + kSub * PARTS > vis_first;
                 float tm[NR][2];
                 bool move = false;
 #pragma unroll
                 for (int z = 0; z < NR; ++z)
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
-                        const float f = crow[z][x] * sc.x;
-                        s[z][x] = fmaf(s[z][x], f, sc.y);
-                        s[z][2 + x] = fmaf(s[z][2 + x], f, sc.y);
-                        if (masked) {
-                            if (key0 + g >= vis[z][x]) s[z][x] = -INFINITY;
-                            if (key0 + g + 8 >= vis[z][x]) s[z][2 + x] = -INFINITY;
+                        float q = -INFINITY;
+#pragma unroll
+                        for (int u = 0; u < PARTS; ++u) {
+                            const float f = crow[z][x] * scs[u].x, lv = scs[u].y;
+                            s[u][z][x] = fmaf(s[u][z][x], f, lv);
+                            s[u][z][2 + x] = fmaf(s[u][z][2 + x], f, lv);
+                            if (masked) {
+                                if (key0 + u * kSub + g >= vis[z][x]) s[u][z][x] = -INFINITY;
+                                if (key0 + u * kSub + g + 8 >= vis[z][x]) s[u][z][2 + x] = -INFINITY;
+                            }
+                            q = fmaxf(q, fmaxf(s[u][z][x], s[u][z][2 + x]));
                         }
-                        float q = fmaxf(s[z][x], s[z][2 + x]);
                         q = fmaxf(q, __shfl_xor_sync(0xffffffffu, q, 4));
                         q = fmaxf(q, __shfl_xor_sync(0xffffffffu, q, 8));
                         tm[z][x] = fmaxf(q, __shfl_xor_sync(0xffffffffu, q, 16));
@@ -429,39 +433,58 @@ kv8_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
                             for (int j = 0; j < NO; ++j) o[z][j][x] *= f, o[z][j][2 + x] *= f;
                         }
                 }
-                uint32_t pf[NR][2];
 #pragma unroll
-                for (int z = 0; z < NR; ++z) {
-                    float p[4];
+                for (int u = 0; u < PARTS; ++u) {
+                    const float vq = scs[u].z;
+                    uint32_t pf[NR][2];
 #pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        const float mu = m[z][x] == -INFINITY ? 0.0f : m[z][x];
-                        p[x] = ex2(s[z][x] - mu);
-                        p[2 + x] = ex2(s[z][2 + x] - mu);
-                        // (a row that sees none of these keys takes nothing from their scale)
-                        if (!masked || key0 < vis[z][x]) l[z][x] = fmaf(p[x] + p[2 + x], sc.z, l[z][x]);
+                    for (int z = 0; z < NR; ++z) {
+                        float p[4];
+#pragma unroll
+                        for (int x = 0; x < 2; ++x) {
+                            const float mu = m[z][x] == -INFINITY ? 0.0f : m[z][x];
+                            p[x] = ex2(s[u][z][x] - mu);
+                            p[2 + x] = ex2(s[u][z][2 + x] - mu);
+                            // (a row that sees none of these keys takes nothing from their scale)
+                            if (!masked || key0 + u * kSub < vis[z][x]) l[z][x] = fmaf(p[x] + p[2 + x], vq, l[z][x]);
+                        }
+                        // rows to the lane groups, keys to the lanes: the B operand
+                        pf[z][0] = movmatrix(pack_half2(p[0], p[1]));
+                        pf[z][1] = movmatrix(pack_half2(p[2], p[3]));
                     }
-                    // rows to the lane groups, keys to the lanes: the B operand
-                    pf[z][0] = movmatrix(pack_half2(p[0], p[1]));
-                    pf[z][1] = movmatrix(pack_half2(p[2], p[3]));
-                }
+                    // V: this lane's keys are 2 c, 2 c + 1, 2 c + 8, 2 c + 9, its
+                    // columns [g DG, (g + 1) DG)
+                    const uint32_t vb = kb0 + C::KV + u * kSub * D;
+                    uint32_t vw[4][D / 32];
 #pragma unroll
-                for (int q = 0; q < D / 32; ++q) {
-                    uint32_t b[2][4];
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const uint32_t x0 = vw[2 * e][q] ^ 0x80808080u, x1 = vw[2 * e + 1][q] ^ 0x80808080u;
-                        const uint32_t lo = __byte_perm(x0, x1, 0x5140), hi = __byte_perm(x0, x1, 0x7362);
-                        b[e][0] = half2_of(lo, 0x4140);
-                        b[e][1] = half2_of(lo, 0x4342);
-                        b[e][2] = half2_of(hi, 0x4140);
-                        b[e][3] = half2_of(hi, 0x4342);
+                    for (int e = 0; e < 4; ++e) {
+                        const int row = 2 * c + (e & 1) + (e >> 1) * 8;
+                        if constexpr (D == 128) {
+                            const uint4 v = lds128(vb + row * D + ((g ^ (row & 7)) << 4));
+                            vw[e][0] = v.x, vw[e][1] = v.y, vw[e][2] = v.z, vw[e][3] = v.w;
+                        } else {
+                            const uint2 v = lds64(vb + row * D + (((g >> 1) ^ ((row >> 1) & 3)) << 4) + (g & 1) * 8);
+                            vw[e][0] = v.x, vw[e][1] = v.y;
+                        }
                     }
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const uint32_t af[4] = {b[0][2 * e], b[0][2 * e + 1], b[1][2 * e], b[1][2 * e + 1]};
+                    for (int q = 0; q < D / 32; ++q) {
+                        uint32_t b[2][4];
 #pragma unroll
-                        for (int z = 0; z < NR; ++z) mma16816(o[z][2 * q + e], af, pf[z][0], pf[z][1]);
+                        for (int e = 0; e < 2; ++e) {
+                            const uint32_t x0 = vw[2 * e][q] ^ 0x80808080u, x1 = vw[2 * e + 1][q] ^ 0x80808080u;
+                            const uint32_t lo = __byte_perm(x0, x1, 0x5140), hi = __byte_perm(x0, x1, 0x7362);
+                            b[e][0] = half2_of(lo, 0x4140);
+                            b[e][1] = half2_of(lo, 0x4342);
+                            b[e][2] = half2_of(hi, 0x4140);
+                            b[e][3] = half2_of(hi, 0x4342);
+                        }
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const uint32_t af[4] = {b[0][2 * e], b[0][2 * e + 1], b[1][2 * e], b[1][2 * e + 1]};
+#pragma unroll
+                            for (int z = 0; z < NR; ++z) mma16816(o[z][2 * q + e], af, pf[z][0], pf[z][1]);
+                        }
                     }
                 }
             }
@@ -699,7 +722,7 @@ extern "C" sq_status_t sq_kv8_attention(const void* Q, sq_dtype_t dt, int64_t T,
     a.G = (int)(Hq / Hkv);
     a.block = (int)block;
     a.block_log2 = block == 16 ? 4 : block == 32 ? 5 : block == 64 ? 6 : 7;
-    a.box = (int)(block < sq::kTile ? block : sq::kTile);
+    a.box = (int)(block < 64 ? block : 64);
     a.max_blocks = (int)max_blocks;
     a.causal = causal != 0;
     a.scale = scale;
