@@ -403,7 +403,7 @@ SQ_API sq_status_t sq_gemm_fp8(const uint8_t* Xq, const uint8_t* Wq, int64_t M, 
  * sq_quantize_weight_fp4: v = fp32(W) * s[k]; sq_quantize_act_fp4: v = fp32(X) /
  *   s[k] (IEEE division); s may be NULL: v = the input. Then per row
  *     NVFP4: qs = 2^(10 - floor(log2 max|v|)) (max|v| below 2^-100 counts as
- *       2^-100), or *static_qs with per_token = 0; u = fl(v * qs); per block
+ *       2^-100), or *static_qs (> 0) with per_token = 0; u = fl(v * qs); per block
  *       b = E4M3(fl(max|u| / 6)), codes = E2M1(fl(u / b)), zero where b is zero
  *     MXFP4: b = 2^(floor(log2 max|v|) - 2) (at least 2^-127), codes = E2M1(v / b)
  *   each conversion to the nearest, ties to even, magnitudes past 448 (6)
@@ -465,8 +465,9 @@ SQ_API sq_status_t sq_gemm_fp4(const uint8_t* Xq, const uint8_t* Xs, const uint8
  *   Q, Y: [T, Hq, D] of dt in {F16, BF16}, token strides ldq, ldy (multiples of
  *   8), 16-byte aligned. Scores, maxima, sums and outputs are fp32; the softmax
  *   weights are rounded to fp16 (2^-11) for the second product.
- *   max_q: the largest number of new tokens of a sequence, or an upper bound; it
- *   chooses between kernels, results do not depend on it being exact.
+ *   max_q: the largest number of new tokens of a sequence; it chooses between the
+ *   kernels for few and for many rows, and any value gives a right result.
+ *   T * Hq < 2^31.
  *   Workspace: SQ_OP_KV8_ATTENTION (M = T, N = Hq, K = D; the size does not depend
  *   on lengths), zeroed once before first use, as for sq_gemm_fp4.
  * ------------------------------------------------------------------------ */

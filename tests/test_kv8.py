@@ -53,7 +53,7 @@ def test_refusals(L):
     ok = [p, 2, 4, 8, 2, 64, 512, p, p, p, p, 8, 16, p, p, 1, p, 4, 4, 0.125, 1, 4, p, 512, p, big, None]
     for at, v, code, text in [(1, 0, 1, "dtype"), (3, 7, 2, "multiple of Hkv"), (5, 32, 2, "head width"),
                               (12, 8, 2, "block must"), (6, 256, 2, "strides"), (6, 516, 3, "aligned"),
-                              (0, None, 1, "null"), (22, None, 1, "null"), (16, None, 1, "null"), (21, -1, 1, "max_q"),
+                              (0, None, 1, "null"), (2, 1 << 28, 2, "2^31"), (22, None, 1, "null"), (16, None, 1, "null"), (21, -1, 1, "max_q"),
                               (24, None, 1, "workspace"), (25, 256, 1, "workspace"), (7, odd, 3, "aligned"),
                               (23, 8, 2, "strides")]:
         bad = list(ok)
@@ -388,6 +388,28 @@ def test_attention_rows_behind_the_last_sequence():
     y = run_attention(batch, q, 0.125, True)
     check_attention(batch, q[:3], 0.125, y=y)
     assert bool((y[3:] == -7).all())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("max_q", [0, 1, 3, 200, 1 << 40])
+def test_attention_with_any_max_q(max_q):
+    batch = ref.Batch([1, 5, 170, 0, 30], [77, 300, 200, 4, 31], 2, 128, 16, seed=11)
+    check_attention(batch, rows16(batch.T, 6, 128, BF, 1), max_q=max_q)
+
+
+@pytest.mark.gpu
+def test_attention_many_sequences():
+    """More sequences than are looked at together (32), with empty ones and prompts among them."""
+    g = np.random.default_rng(12)
+    new = g.integers(0, 3, 150)
+    new[[3, 40, 41, 130]] = [90, 33, 70, 65]
+    lens = np.maximum(new, g.integers(0, 200, 150))
+    batch = ref.Batch(new.tolist(), lens.tolist(), 1, 64, 16, seed=12)
+    check_attention(batch, rows16(batch.T, 4, 64, FP, 1))
+    batch.new = [min(n, 1) for n in batch.new]
+    batch.cu = np.concatenate([[0], np.cumsum(batch.new)]).astype(np.int32)
+    batch.T = int(batch.cu[-1])
+    check_attention(batch, rows16(batch.T, 4, 64, FP, 2))
 
 
 @pytest.mark.gpu

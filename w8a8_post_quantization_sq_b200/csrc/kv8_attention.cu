@@ -692,8 +692,7 @@ extern "C" sq_status_t sq_kv8_attention(const void* Q, sq_dtype_t dt, int64_t T,
     SQ_REQUIRE(Hq > 0 && Hq % Hkv == 0 && Hq <= 65535, SQ_ERR_UNSUPPORTED_SHAPE,
                "%s: Hq must be a multiple of Hkv", name);
     SQ_REQUIRE(ldq >= Hq * D && ldy >= Hq * D, SQ_ERR_UNSUPPORTED_SHAPE, "%s: token strides must be >= Hq * D", name);
-    SQ_REQUIRE(T * (Hq / Hkv) < (1ll << 31) - 16 && Hkv * block < (1ll << 31), SQ_ERR_UNSUPPORTED_SHAPE,
-               "%s: too many rows", name);
+    SQ_REQUIRE(T * Hq < (1ll << 31) - 65536, SQ_ERR_UNSUPPORTED_SHAPE, "%s: tokens x heads must be < 2^31", name);
     SQ_REQUIRE(max_q >= 0, SQ_ERR_INVALID_ARG, "%s: max_q must be >= 0", name);
     if (T == 0 || B == 0) return SQ_OK;
     SQ_REQUIRE(Q && Kc && Vc && kqs && vqs && cu_q && seq_lens && block_table && Y, SQ_ERR_INVALID_ARG,
