@@ -228,25 +228,45 @@ __device__ __forceinline__ void epi_chunk(const Params& p, const uint32_t* r, in
                                     pack2<OUT>(y[8 * e + 4], y[8 * e + 5]), pack2<OUT>(y[8 * e + 6], y[8 * e + 7]));
         }
         __syncwarp();
-        const int part = lane & 3;
+        if (p.vec_store) {
+            const int part = lane & 3;
 #pragma unroll
-        for (int it = 0; it < 4; ++it) {
-            const int rr = it * 8 + (lane >> 2);
-            const int64_t grow = (int64_t)row0 + rr;
-            const int col = col0 + 16 * hh + part * EPV;
-            const uint4 v = *reinterpret_cast<const uint4*>(stg + rr * kStgRow + part * 16);
-            if (grow < p.M && col < p.N) {
-                uint8_t* out = static_cast<uint8_t*>(p.Y) + (grow * p.ldy + col) * EB;
-                if (p.vec_store && col + EPV <= p.N) {
-                    *reinterpret_cast<uint4*>(out) = v;
-                } else {
-                    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+            for (int it = 0; it < 4; ++it) {
+                const int rr = it * 8 + (lane >> 2);
+                const int64_t grow = (int64_t)row0 + rr;
+                const int col = col0 + 16 * hh + part * EPV;
+                const uint4 v = *reinterpret_cast<const uint4*>(stg + rr * kStgRow + part * 16);
+                if (grow < p.M && col < p.N) {
+                    uint8_t* out = static_cast<uint8_t*>(p.Y) + (grow * p.ldy + col) * EB;
+                    if (col + EPV <= p.N) {
+                        *reinterpret_cast<uint4*>(out) = v;
+                    } else {
+                        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-                    for (int e = 0; e < EPV; ++e)
-                        if (col + e < p.N) {
-                            if constexpr (OUT == kOutF32) reinterpret_cast<uint32_t*>(out)[e] = w[e];
-                            else reinterpret_cast<uint16_t*>(out)[e] = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
-                        }
+                        for (int e = 0; e < EPV; ++e)
+                            if (col + e < p.N) {
+                                if constexpr (OUT == kOutF32) reinterpret_cast<uint32_t*>(out)[e] = w[e];
+                                else reinterpret_cast<uint16_t*>(out)[e] = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
+                            }
+                    }
+                }
+            }
+        } else {
+            // rows that start anywhere: an element a lane, neighbours together
+            constexpr int W = 64 / EB;      // elements of a staged row
+            constexpr int RPI = 32 / W;     // rows a store
+            const int cc = lane % W;
+            const int col = col0 + 16 * hh + cc;
+#pragma unroll 4
+            for (int rr = lane / W; rr < 32; rr += RPI) {
+                const int64_t grow = (int64_t)row0 + rr;
+                if (grow < p.M && col < p.N) {
+                    if constexpr (OUT == kOutF32)
+                        static_cast<uint32_t*>(p.Y)[grow * p.ldy + col] =
+                            *reinterpret_cast<const uint32_t*>(stg + rr * kStgRow + cc * 4);
+                    else
+                        static_cast<uint16_t*>(p.Y)[grow * p.ldy + col] =
+                            *reinterpret_cast<const uint16_t*>(stg + rr * kStgRow + cc * 2);
                 }
             }
         }
