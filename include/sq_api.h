@@ -418,8 +418,12 @@ SQ_API sq_status_t sq_gemm_fp8(const uint8_t* Xq, const uint8_t* Wq, int64_t M, 
  *   the tensor cores' fp32 sum of the products code_x b_x code_w b_w. qs_x: [M]
  *   (x_per_token), [1] or NULL (1); qs_w: [N] (w_per_channel), [1] or NULL;
  *   bias: [N] fp32 or NULL. K % 32 == 0; codes and scales 16-byte aligned.
- *   Workspace: SQ_OP_GEMM_FP4 (256 bytes for every shape), zeroed once before
- *   first use; it holds the status word of the bounded waits.
+ *   Workspace: SQ_OP_GEMM_FP4, zeroed once before first use; it holds the status
+ *   word and, for shapes whose last wave of tiles would leave much of the device
+ *   idle, arrival counters (at the same bytes for every shape, zero again after
+ *   every completed call) and the parked sums of that wave's split k-loops. A
+ *   smaller one (at least 256 bytes) is accepted and splits nothing. Calls sharing
+ *   one must not run concurrently.
  * ------------------------------------------------------------------------ */
 SQ_API size_t sq_fp4_scale_bytes(sq_fp4_t fmt, int64_t rows, int64_t K);
 SQ_API sq_status_t sq_quantize_weight_fp4(const void* W, sq_dtype_t dt, int64_t N, int64_t K, const float* s,

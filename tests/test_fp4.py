@@ -278,6 +278,44 @@ def test_gemm_many_tiles(M, N, K, fmt):
     sq.sq_workspace_status(ws)
 
 
+def random_operand(rows, K, fmt, seed):
+    """Any codes, any block scales of moderate size, row scales for NVFP4; and what they stand for."""
+    g = np.random.default_rng(seed)
+    codes = g.integers(0, 16, (rows, K), dtype=np.uint8)
+    byte = g.integers(0x28, 0x50, (rows, K // ref.BLOCK[fmt])) if fmt == 0 else g.integers(122, 131, (rows, K // 32))
+    q = 2.0 ** g.integers(-3, 4, rows) if fmt == 0 else None
+    byte = byte.astype(np.uint8)
+    dev = (torch.from_numpy(ref.pack(codes)).cuda(), torch.from_numpy(ref.tile(byte)).cuda(),
+           None if q is None else torch.from_numpy(q).float().cuda())
+    v = torch.tensor(ref.GRID, device="cuda")[torch.from_numpy(codes & 7).cuda().int()]
+    v = torch.where(torch.from_numpy(codes & 8).cuda() > 0, -v, v)
+    v *= torch.from_numpy(ref.scale_value(byte, fmt)).cuda().repeat_interleave(ref.BLOCK[fmt], 1)
+    return dev, v if q is None else v / torch.from_numpy(q).cuda()[:, None]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("M,N,K", [(2560, 2560, 12288), (2500, 2490, 12320), (1024, 7168, 16384)])
+def test_gemm_split_last_wave(M, N, K, fmt):
+    """Shapes whose last wave is cut by k-blocks: with and without room for it, twice, and counters zero again."""
+    (xq, xs, qx), xv = random_operand(M, K, fmt, 1)
+    (wq, wsc, qw), wv = random_operand(N, K, fmt, 2)
+    ws = sq.workspace(sq.SQ_OP_GEMM_FP4, M, N, K)
+    assert ws.numel() > 256
+    bias = torch.randn(N, generator=torch.Generator().manual_seed(5)).cuda()
+    for dt, b in ((torch.bfloat16, bias), (torch.float32, None)):
+        ys = []
+        for use in (ws, ws, ws[:256]):
+            y = torch.empty((M, N), dtype=dt, device="cuda")
+            sq.sq_gemm_fp4(xq, xs, wq, wsc, fmt, qx, qw, b, y, use)
+            ys.append(y)
+        check_gemm(ys[0], xv, wv, b, K)
+        check_gemm(ys[2], xv, wv, b, K)
+        assert torch.equal(ys[0], ys[1])
+        assert int(ws[: 256 + 128 * 2 * 8 * 4].sum()) == int(ws[12:16].sum())  # only the region's size is noted
+    sq.sq_workspace_status(ws)
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("dt", DTYPES)
 @pytest.mark.parametrize("ldy", [1008, 1003])
@@ -328,12 +366,13 @@ def test_gemm_nan_stays_in_its_row():
 @pytest.mark.gpu
 def test_gemm_workspace_and_repeats():
     """One workspace for shapes with and without a split, in turn; equal bits every time; a small workspace."""
-    shapes = [(16, 4096, 4096), (1, 1024, 8192), (300, 512, 1024), (8, 128, 16384), (16, 4096, 4096)]
+    shapes = [(16, 4096, 4096), (1, 1024, 8192), (300, 512, 1024), (2560, 2560, 12288), (8, 128, 16384),
+              (16, 4096, 4096)]
     ws = torch.zeros(max(sq.sq_workspace_size(sq.SQ_OP_GEMM_FP4, *s) for s in shapes), dtype=torch.uint8, device="cuda")
     small = torch.zeros(256, dtype=torch.uint8, device="cuda")
     for M, N, K in shapes:
-        (xq, xs, qx), xv = operand(M, K, 0, 1)
-        (wq, wsc, qw), wv = operand(N, K, 0, 2)
+        (xq, xs, qx), xv = random_operand(M, K, 0, 1)
+        (wq, wsc, qw), wv = random_operand(N, K, 0, 2)
         ys = []
         for use in (ws, ws, small):
             y = torch.empty((M, N), device="cuda")
@@ -341,7 +380,7 @@ def test_gemm_workspace_and_repeats():
             check_gemm(y, xv, wv, None, K)
             ys.append(y)
         assert torch.equal(ys[0], ys[1])
-        assert int(ws.sum()) == 0
+        assert int(ws[256 : 256 + 8192].sum()) == 0  # counters are zero again
         sq.sq_workspace_status(ws)
 
 

@@ -21,6 +21,11 @@
 //     scales' two sets of 48 (24) columns exceed the 512 of tensor memory, so the
 //     accumulators share 96 (48): the epilogue reads the shared columns first
 //     and hands them back, and the next tile's MMAs start while the rest is read;
+//   - a last wave of pair tiles that is not full: its tiles are cut by k-blocks
+//     into one contiguous range per pair, run before the whole tiles; a piece's
+//     sums are parked in the workspace, and the piece that completes a tile adds
+//     them in range order (1024 x 7168 x 28672, 112 tiles on 74 pairs: 106 us in
+//     two waves, 92 so);
 //   - few tiles (decode batches): a kernel of its own, one 128 x 128 tile (or one
 //     part of its k-loop) per CTA, two CTAs per SM; the parts of a tile are a
 //     cluster, which adds them up through its shared memory, in part order.
@@ -93,7 +98,6 @@ struct Cfg {
 struct Params {
     int M, N, K;
     int num_m, num_n, num_kb;
-    int tiles;
     int group_m;
     int vec_store, tma_store;
     const float* qs_x;
@@ -103,6 +107,54 @@ struct Params {
     void* Y;
     int64_t ldy;
     int* status;
+    // the last wave's split: the first dp_tiles tiles run whole; the k-blocks of
+    // the other sk_tiles, sk_iters in all, are dealt to the pairs
+    int dp_tiles, sk_tiles, sk_iters, sk_units;
+    int sk_cnt_bytes;
+    int* sk_cnt;     // [sk_tiles][CG][kEpiWarps] k-blocks counted in (zero between launches)
+    float* sk_part;  // [CTA][2][kEpiWarps][NCH][8][32] float4
+};
+
+// First k-block of unit c's range, and the unit whose range holds k-block x
+// (every unit has at least one: sk_iters >= sk_units).
+__device__ __forceinline__ int sk_start(int c, const Params& p) {
+    return (int)((int64_t)c * p.sk_iters / p.sk_units);
+}
+__device__ __forceinline__ int sk_owner(int x, const Params& p) {
+    return (int)((((int64_t)x + 1) * p.sk_units + p.sk_iters - 1) / p.sk_iters - 1);
+}
+
+// A unit's work, the same sequence for all its roles: the pieces of its range
+// (the part inside one tile each; slot 0 for the first, 1 for the last, -1 where
+// a piece is a whole tile), then its whole tiles.
+template <bool SK, int CG>
+struct Segments {
+    int tile_dp, it, end;
+    bool first;
+    __device__ __forceinline__ explicit Segments(const Params& p) {
+        tile_dp = blockIdx.x / CG;
+        it = SK ? sk_start(blockIdx.x / CG, p) : 0;
+        end = SK ? sk_start(blockIdx.x / CG + 1, p) : 0;
+        first = true;
+    }
+    __device__ __forceinline__ bool next(const Params& p, int& tile, int& k0, int& k1, int& slot) {
+        if (SK && it < end) {
+            const int u = it / p.num_kb;
+            k0 = it - u * p.num_kb;
+            k1 = min(p.num_kb, k0 + (end - it));
+            tile = p.dp_tiles + u;
+            slot = (k0 == 0 && k1 == p.num_kb) ? -1 : (first ? 0 : 1);
+            first = false;
+            it += k1 - k0;
+            return true;
+        }
+        tile = tile_dp;
+        k0 = 0;
+        k1 = p.num_kb;
+        slot = -1;
+        tile_dp += gridDim.x / CG;
+        return tile < p.dp_tiles;
+    }
 };
 
 __device__ __forceinline__ void tile_coords(int tile, const Params& p, int bm, int bn, int& m0, int& n0) {
@@ -274,7 +326,7 @@ __device__ __forceinline__ void epi_chunk(const Params& p, const uint32_t* r, in
     }
 }
 
-template <int FMT, int BN, int CG, int OUT>
+template <int FMT, int BN, int CG, int OUT, bool SK>
 __global__ void __launch_bounds__(kThreads, 1)
 gemm_fp4_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ CUtensorMap tmap_b,
                 const __grid_constant__ CUtensorMap tmap_sa, const __grid_constant__ CUtensorMap tmap_sb,
@@ -339,20 +391,22 @@ gemm_fp4_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constan
     pdl_wait();
     pdl_trigger();
 
-    const int first = blockIdx.x / CG, step = gridDim.x / CG, items = p.tiles;  // this CTA's (or pair's) tiles
+    if (SK && blockIdx.x == 0 && threadIdx.x == 0) p.status[3] = p.sk_cnt_bytes;
+    Segments<SK, CG> seg(p);
+    int tile, k0, k1, slot;
     if (warp == 0) {
         if (lane == 0) {
             // ---------------------------------------------------- TMA producer
             int stage = 0;
             uint32_t phase = 0, issued = 0, issued_phase = 0;
             bool ok = true;
-            for (int w = first; ok && w < items; w += step) {
+            while (ok && seg.next(p, tile, k0, k1, slot)) {
                 int m0, n0;
-                tile_coords(w, p, BM * CG, BN, m0, n0);
+                tile_coords(tile, p, BM * CG, BN, m0, n0);
                 const int gn = n0 / 128;
                 m0 += (int)rank * BM;
                 n0 += (int)rank * (BN / CG);
-                for (int kb = 0; kb < p.num_kb; ++kb) {
+                for (int kb = k0; kb < k1; ++kb) {
                     if (!wait_fast(empty_bar(stage), phase ^ 1u, abort_flag, p.status, 0x8E1)) {
                         ok = false;
                         break;
@@ -385,7 +439,7 @@ gemm_fp4_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constan
             int stage = 0, local = 0;
             uint32_t phase = 0, set = 0;
             bool ok = true;
-            for (int w = first; ok && w < items; w += step, ++local) {
+            for (; ok && seg.next(p, tile, k0, k1, slot); ++local) {
                 const int acc = local & 1;
                 // accumulators that share columns: the previous tile's shared
                 // columns (and all of the tile before it) have been read; else
@@ -398,7 +452,7 @@ gemm_fp4_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constan
                 }
                 tc_fence_after();
                 const uint32_t d_tmem = tmem_base + (acc ? C::ACC1 : 0u);
-                for (int kb = 0; kb < p.num_kb; ++kb) {
+                for (int kb = k0; kb < k1; ++kb) {
                     if (!wait_fast(full_bar(stage), phase, abort_flag, p.status, 0x8E3) ||
                         !wait_fast(sready_bar(stage), phase, abort_flag, p.status, 0x8E5)) {
                         ok = false;
@@ -417,7 +471,7 @@ gemm_fp4_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constan
                         const int c = FMT == SQ_NVFP4 ? k : k >> 1;       // scale tile of this MMA
                         const int sf = FMT == SQ_NVFP4 ? 0 : (k & 1) * 2;  // first byte of its words
                         umma_fp4<FMT, CG>(d_tmem, sdesc(a_addr + k * (UMMA_K / 2)), sdesc(b_addr + k * (UMMA_K / 2)),
-                                          C::idesc(sf), sfa + c * 4, sfb + c * C::NG * 4, (kb != 0 || k != 0) ? 1u : 0u);
+                                          C::idesc(sf), sfa + c * 4, sfb + c * C::NG * 4, (kb != k0 || k != 0) ? 1u : 0u);
                     }
                     umma_commit<CG>(empty_bar(stage));
                     if (++stage == STAGES) stage = 0, phase ^= 1u;
@@ -436,8 +490,8 @@ gemm_fp4_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constan
         int stage = 0, before = -2;  // `before`: the stage two stages ago, whose MMAs read this stage's set
         uint32_t phase = 0, before_phase = 0, set = 0;
         bool ok = true;
-        for (int w = first; ok && w < items; w += step) {
-            for (int kb = 0; kb < p.num_kb; ++kb) {
+        while (ok && seg.next(p, tile, k0, k1, slot)) {
+            for (int kb = k0; kb < k1; ++kb) {
                 ok = wait_fast(sfull_bar(stage), phase, abort_flag, p.status, 0x8E6);
                 if (ok && before >= 0) ok = wait_fast(empty_bar(before), before_phase, abort_flag, p.status, 0x8E7);
                 ok = __all_sync(0xffffffffu, ok);
@@ -486,9 +540,9 @@ gemm_fp4_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constan
             }
         };
         int local = 0;
-        for (int w = first; w < items; w += step, ++local) {
+        for (; seg.next(p, tile, k0, k1, slot); ++local) {
             int m0, n0;
-            tile_coords(w, p, BM * CG, BN, m0, n0);
+            tile_coords(tile, p, BM * CG, BN, m0, n0);
             m0 += (int)rank * BM;
             const int c_base = n0 + half * HC;
             const int row0 = m0 + q * 32;
@@ -528,6 +582,61 @@ gemm_fp4_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constan
             // shared columns first: the upper half's last chunks of the first
             // accumulator, the lower half's first ones of the second
             const int turn = C::OVERLAP && acc == 0 && half == 1 ? NCH - C::SHARED : 0;
+            if constexpr (SK) {
+                if (slot >= 0) {
+                    // a piece: park the sums; the one that completes the tile's
+                    // k-blocks adds every piece's in range order
+                    const int wr = warp - 2;
+                    constexpr int REGION = NCH * 8 * 32;  // float4 per warp
+                    float4* parts = reinterpret_cast<float4*>(p.sk_part);
+                    float4* mine = parts + ((int64_t)(blockIdx.x * 2 + slot) * kEpiWarps + wr) * REGION;
+#pragma unroll 1
+                    for (int i = 0; i < NCH; ++i) {
+                        const int c = (i + turn) & (NCH - 1);
+                        tmem_ld32(t_row + (uint32_t)(c * 32), r);
+                        if (shares && i == C::SHARED - 1) release_acc(acc);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            __stcg(mine + (c * 8 + e) * 32 + lane,
+                                   make_float4(__uint_as_float(r[4 * e]), __uint_as_float(r[4 * e + 1]),
+                                               __uint_as_float(r[4 * e + 2]), __uint_as_float(r[4 * e + 3])));
+                    }
+                    __threadfence();
+                    __syncwarp();
+                    const int u = tile - p.dp_tiles;
+                    int before = 0;
+                    int* cnt = p.sk_cnt + (u * CG + (int)rank) * kEpiWarps + wr;
+                    if (lane == 0) before = atomicAdd(cnt, k1 - k0);
+                    before = __shfl_sync(0xffffffffu, before, 0);
+                    if (before + (k1 - k0) != p.num_kb) continue;
+                    __threadfence();
+                    if (lane == 0) *cnt = 0;  // ready for the next launch
+                    const int x0 = u * p.num_kb;
+                    const int c_lo = sk_owner(x0, p), c_hi = sk_owner(x0 + p.num_kb - 1, p);
+#pragma unroll 1
+                    for (int c = 0; c < NCH; ++c) {
+                        if (row0 >= p.M || c_base + c * 32 >= p.N) break;
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) r[e] = 0u;
+#pragma unroll 1
+                        for (int cc = c_lo; cc <= c_hi; ++cc) {
+                            const int sl = sk_start(cc, p) >= x0 ? 0 : 1;
+                            const float4* src =
+                                parts + ((int64_t)((cc * CG + (int)rank) * 2 + sl) * kEpiWarps + wr) * REGION;
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) {
+                                const float4 v = __ldcg(src + (c * 8 + e) * 32 + lane);
+                                r[4 * e] = __float_as_uint(__uint_as_float(r[4 * e]) + v.x);
+                                r[4 * e + 1] = __float_as_uint(__uint_as_float(r[4 * e + 1]) + v.y);
+                                r[4 * e + 2] = __float_as_uint(__uint_as_float(r[4 * e + 2]) + v.z);
+                                r[4 * e + 3] = __float_as_uint(__uint_as_float(r[4 * e + 3]) + v.w);
+                            }
+                        }
+                        epi_chunk<OUT>(p, r, c * 32, c_base + c * 32, row0, rx, rw_w, bias_w, stg, lane, &tmap_y);
+                    }
+                    continue;
+                }
+            }
 #pragma unroll 1
             for (int i = 0; i < NCH; ++i) {
                 const int c = (i + turn) & (NCH - 1);
@@ -834,7 +943,15 @@ bool make_map_scales(CUtensorMap* m, const uint8_t* base, int64_t groups, int64_
 struct Plan {
     bool pairs = false;
     int tiles = 0, splits = 1, grid = 0;
+    int sk_tiles = 0;     // trailing pair tiles that are cut by k-blocks
+    size_t sk_bytes = 0;  // their counters and parked sums
 };
+
+// Counters at a fixed place for every shape: one per warp region of the split
+// tiles, of which there are fewer than pairs.
+constexpr int kMaxSplitTiles = 128;
+constexpr size_t kSkCntBytes = (size_t)kMaxSplitTiles * 2 * kEpiWarps * sizeof(int);
+static_assert(kSkCntBytes % 256 == 0, "the parked sums start 256-byte aligned");
 
 Plan plan_fp4(int64_t M, int64_t N, int64_t K) {
     Plan pl;
@@ -851,6 +968,18 @@ Plan plan_fp4(int64_t M, int64_t N, int64_t K) {
         pl.tiles = (int)ptiles;
         const int64_t pairs = sms / 2;
         pl.grid = (int)(2 * (ptiles < pairs ? ptiles : pairs));
+        // Split where the last wave would be at most three quarters full and the
+        // waves under 95 % busy, for k-loops of 48 blocks or more, with eight or
+        // more for every pair: parking and adding the pieces takes about 10 us.
+        // Whole / split (us): 1024 x 7168 x 28672 (112 blocks) 106 / 92, 4096 x
+        // 12288 x 12288 (48) 255 / 253, 1024 x 7168 x 7168 (28) 31.6 / 33.8, 2048 x
+        // 4096 x 4096 (16) 21.4 / 31.2.
+        const int64_t rem = ptiles % pairs, waves = (ptiles + pairs - 1) / pairs;
+        if (ptiles > pairs && rem > 0 && 4 * rem <= 3 * pairs && 20 * ptiles < 19 * waves * pairs &&
+            kb >= 48 && rem * kb >= 8 * pairs && rem * kb < (1ll << 31) && rem <= kMaxSplitTiles) {
+            pl.sk_tiles = (int)rem;
+            pl.sk_bytes = kSkCntBytes + (size_t)pl.grid * 2 * BM * 256 * sizeof(float);
+        }
         return pl;
     }
     pl.tiles = (int)tiles;
@@ -893,7 +1022,7 @@ sq_status_t launch_pairs(const char* name, const Call& c, const Plan& pl, Params
     const int64_t per = (int64_t)BM * CG * c.K / 2;
     const int64_t g = (48ll << 20) / per;
     p.group_m = (int)(g < 1 ? 1 : g > p.num_m ? p.num_m : g);
-    auto fn = gemm_fp4_kernel<FMT, BN, CG, OUT>;
+    auto fn = p.sk_tiles > 0 ? gemm_fp4_kernel<FMT, BN, CG, OUT, true> : gemm_fp4_kernel<FMT, BN, CG, OUT, false>;
     if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM_ALLOC) != cudaSuccess)
         return check_launch(name);
     launch_pdl_cluster(fn, dim3(pl.grid), dim3(kThreads), C::SMEM_ALLOC, stream, 2, ta, tb, tsa, tsb, ty, p);
@@ -938,8 +1067,8 @@ sq_status_t launch_out(const char* name, const Call& c, const Plan& pl, Params& 
 }  // namespace
 
 size_t gemm_fp4_workspace_bytes(int64_t M, int64_t N, int64_t K) {
-    (void)M, (void)N, (void)K;
-    return kStatusBytes;  // the status word of the bounded waits
+    if (M <= 0 || N <= 0 || K <= 0) return kStatusBytes;
+    return kStatusBytes + plan_fp4(M, N, K).sk_bytes;
 }
 
 }  // namespace sq
@@ -971,7 +1100,6 @@ extern "C" sq_status_t sq_gemm_fp4(const uint8_t* Xq, const uint8_t* Xs, const u
     p.N = (int)N;
     p.K = (int)K;
     p.num_kb = (int)((K + sq::BK - 1) / sq::BK);
-    p.tiles = pl.tiles;
     p.vec_store = sq::aligned16(Y) && (ldy * eb) % 16 == 0;
     p.qs_x = qs_x;
     p.qs_w = qs_w;
@@ -981,6 +1109,15 @@ extern "C" sq_status_t sq_gemm_fp4(const uint8_t* Xq, const uint8_t* Xs, const u
     p.Y = Y;
     p.ldy = ldy;
     p.status = static_cast<int*>(workspace);
+    // a workspace without room for the split runs whole tiles only
+    p.sk_tiles = ws_bytes >= sq::kStatusBytes + pl.sk_bytes ? pl.sk_tiles : 0;
+    p.dp_tiles = pl.tiles - p.sk_tiles;
+    p.sk_iters = p.sk_tiles * p.num_kb;
+    p.sk_units = pl.grid / 2;
+    p.sk_cnt_bytes = (int)sq::kSkCntBytes;
+    uint8_t* after = static_cast<uint8_t*>(workspace) + sq::kStatusBytes;
+    p.sk_cnt = reinterpret_cast<int*>(after);
+    p.sk_part = reinterpret_cast<float*>(after + sq::kSkCntBytes);
     const sq::Call c = {Xq, Xs, Wq, Ws, M, N, K, out_dt};
     cudaStream_t s = sq::as_cuda(stream);
     return fmt == SQ_NVFP4 ? sq::launch_out<SQ_NVFP4>(name, c, pl, p, s) : sq::launch_out<SQ_MXFP4>(name, c, pl, p, s);
