@@ -413,6 +413,15 @@ def test_attention_many_sequences():
 
 
 @pytest.mark.gpu
+def test_prompts_of_half_a_block_of_rows():
+    """Several blocks of rows to an SM, one after another, all (or only some) with rows in their first half alone."""
+    lens = np.random.default_rng(13).integers(700, 1000, 64)
+    for new in ([70] * 64, [70, 300] * 32):
+        batch = ref.Batch(new, lens.tolist(), 8, 64, 16, seed=13)
+        check_attention(batch, rows16(batch.T, 8, 64, BF, 1))
+
+
+@pytest.mark.gpu
 def test_attention_same_bits_every_time():
     """One workspace for batches of different lengths in turn; equal bits; the counters are zero again."""
     ws = sq.workspace(sq.SQ_OP_KV8_ATTENTION, 64, 16, 128)

@@ -96,6 +96,14 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
         "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
         : "memory");
 }
+// One lane of a converged warp: the MMA warp runs whole and its elected lane
+// issues (216 -> 210 us at 2 prompts of some 1400 tokens, 32 heads, against a
+// single lane in the role).
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(p));
+    return p != 0;
+}
 // 16 columns, with the wait in the same statement.
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t* r) {
     asm volatile(
@@ -105,6 +113,18 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t* r) {
           "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
         : "r"(taddr)
         : "memory");
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float y;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+    return y;
+}
+__device__ __forceinline__ float max3(uint32_t a, uint32_t b, uint32_t c) {
+    return max3(__uint_as_float(a), __uint_as_float(b), __uint_as_float(c));
+}
+// 16 bytes to shared memory (zeros without `live`), not waited for.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool live) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
@@ -264,37 +284,61 @@ kv8_prefill_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_const
         const uint32_t quarter = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t t_s = tmem + quarter + (uint32_t)(x * 128), t_o = tmem + quarter + C::O_COL + (uint32_t)(x * D);
         uint32_t s_phase = 0, o_phase = 0;
-        // this thread's row of the item, and its q on the way
+        // The warp's 32 rows of q are copied to their places in the Q tile, 16 bytes a
+        // lane and whole rows an access, and then scaled in place by a thread per row.
+        // (Through registers, a row a lane, an access touched 32 lines: 8000 cycles
+        // per item.)
+        constexpr int LPR = D / 8, RPI = 32 / LPR;
+        const uint32_t q_tile = sbase + C::Q_OFF + x * C::TILE;
+        // 16 bytes `u` of row r (halves of 64 elements, swizzled)
+        auto unit_of = [&](int r, int u) { return (uint32_t)((u >> 3) * C::HALF + r * 128 + (((u & 7) ^ (r & 7)) << 4)); };
         Item it = {};
-        bool live;
-        int vis;  // keys that the row sees (rows past the end: all, computed and not written)
-        T* y;
-        uint4 w[D / 8];
+        int blk0 = -1, blk1 = -1;
+        // lane e < 8 looks after the scales of keys 16 e .. of a key tile: the block
+        // number two tiles ahead, the scales one
+        auto block_of = [&](int j) {
+            const int key = j * kKeys + (lane & 7) * 16;
+            return key < it.vis ? __ldg(a.table + (int64_t)it.b * a.ldb + (key >> a.block_log2)) : -1;
+        };
         auto fetch = [&]() {
-            const int rows = it.n * a.G;
-            const int r = it.r0 + x * kTileRows + row;
-            live = r < rows;
-            const int i = live ? r / a.G : 0;
-            const int64_t head = (int64_t)(it.h * a.G + (live ? r - i * a.G : 0)) * D;
-            const T* q = static_cast<const T*>(a.Q) + (it.lo + i) * a.ldq + head;
-            y = static_cast<T*>(a.Y) + (it.lo + i) * a.ldy + head;
-            vis = !live ? INT_MAX : a.causal ? max(min(it.len - it.n + i + 1, it.len), 0) : it.len;
-#pragma unroll
-            for (int e = 0; e < D / 8; ++e) w[e] = live ? ldg_nc_v4(q + 8 * e) : make_uint4(0, 0, 0, 0);
+            blk0 = block_of(0);
+            blk1 = block_of(1);
+            const int rows = it.n * a.G, di = RPI / a.G, dg = RPI - di * a.G;
+            int rl = (warp & 3) * 32 + lane / LPR;
+            int r = it.r0 + x * kTileRows + rl, i = r / a.G, g = r - i * a.G;
+            const T* q = static_cast<const T*>(a.Q) + it.lo * a.ldq + (int64_t)it.h * a.G * D + lane % LPR * 8;
+#pragma unroll 1
+            for (int e = 0; e < 32 / RPI; ++e) {
+                cp_async16(q_tile + unit_of(rl, lane % LPR), r < rows ? q + i * a.ldq + g * D : a.Q, r < rows);
+                rl += RPI;
+                r += RPI;
+                i += di;
+                g += dg;
+                if (g >= a.G) g -= a.G, ++i;
+            }
         };
         bool more = take_item(it);
         if (more) fetch();
 #pragma unroll 1
         while (more) {
+            const int rows = it.n * a.G, r = it.r0 + x * kTileRows + row;
+            const bool live = r < rows;
+            const int i = live ? r / a.G : 0;
+            T* const y = static_cast<T*>(a.Y) + (it.lo + i) * a.ldy + (int64_t)(it.h * a.G + (live ? r - i * a.G : 0)) * D;
+            // keys that the row sees (rows past the end: all, computed and not written)
+            const int vis = !live ? INT_MAX : a.causal ? max(min(it.len - it.n + i + 1, it.len), 0) : it.len;
             // Q: scaled by a power of two per row to [1, 2), the score scale's
-            // sign in it, as fp16 to the swizzled tile
+            // sign in it, as fp16
             float crow;
             {
+                asm volatile("cp.async.wait_all;" ::: "memory");
+                __syncwarp();
                 uint32_t m2 = 0;
-#pragma unroll
+#pragma unroll 8
                 for (int e = 0; e < D / 8; ++e) {
-                    m2 = __vmaxu2(m2, __vmaxu2(w[e].x & 0x7fff7fffu, w[e].y & 0x7fff7fffu));
-                    m2 = __vmaxu2(m2, __vmaxu2(w[e].z & 0x7fff7fffu, w[e].w & 0x7fff7fffu));
+                    const uint4 w = *reinterpret_cast<const uint4*>(smem + C::Q_OFF + x * C::TILE + unit_of(row, e));
+                    m2 = __vmaxu2(m2, __vmaxu2(w.x & 0x7fff7fffu, w.y & 0x7fff7fffu));
+                    m2 = __vmaxu2(m2, __vmaxu2(w.z & 0x7fff7fffu, w.w & 0x7fff7fffu));
                 }
                 float top[8];
                 unpack<T>(make_uint4(max(m2 & 0xffffu, m2 >> 16), 0, 0, 0), top);
@@ -302,27 +346,19 @@ kv8_prefill_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_const
                 const float down = copysignf(__uint_as_float((254u - field) << 23), a.scale);
                 // (never 0: a masked score is -inf before it is multiplied)
                 crow = fmaxf(fabsf(a.scale) * kLog2e * __uint_as_float(field << 23), 1.17549435e-38f);
-                uint8_t* base = smem + C::Q_OFF + x * C::TILE + row * 128;
-#pragma unroll
+#pragma unroll 4
                 for (int e = 0; e < D / 8; ++e) {
+                    uint4* at = reinterpret_cast<uint4*>(smem + C::Q_OFF + x * C::TILE + unit_of(row, e));
                     float v[8];
-                    unpack<T>(w[e], v);
-                    *reinterpret_cast<uint4*>(base + (e >> 3) * C::HALF + (((e & 7) ^ (row & 7)) << 4)) =
-                        make_uint4(pack_half2(v[0] * down, v[1] * down), pack_half2(v[2] * down, v[3] * down),
-                                   pack_half2(v[4] * down, v[5] * down), pack_half2(v[6] * down, v[7] * down));
+                    unpack<T>(*at, v);
+                    *at = make_uint4(pack_half2(v[0] * down, v[1] * down), pack_half2(v[2] * down, v[3] * down),
+                                     pack_half2(v[4] * down, v[5] * down), pack_half2(v[6] * down, v[7] * down));
                 }
             }
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(q_ready(x));
-            const int32_t* table = a.table + (int64_t)it.b * a.ldb;
-            // lane e < 8 looks after the scales of keys 16 e .. of a tile: the block
-            // number two tiles ahead, the scales one
-            auto block_of = [&](int j) {
-                const int key = j * kKeys + (lane & 7) * 16;
-                return key < it.vis ? __ldg(table + (key >> a.block_log2)) : -1;
-            };
             auto scales_of = [&](int blk) {
                 float2 s = make_float2(__uint_as_float(0x7fffffffu), __uint_as_float(0x7fffffffu));
                 if (blk >= 0 && blk < a.num_blocks) {
@@ -333,8 +369,8 @@ kv8_prefill_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_const
             };
             const int tiles = it.tiles[x];
             float m = -INFINITY, l = 0.0f;
-            int next_blk = block_of(1);
-            float2 next = scales_of(block_of(0));
+            int next_blk = blk1;
+            float2 next = scales_of(blk0);
 #pragma unroll 1
             for (int j = 0; j < tiles; ++j) {
                 const float my_k = __frcp_rn(next.x), my_v = next.y, my_lv = -__log2f(next.y);
@@ -355,36 +391,37 @@ kv8_prefill_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_const
                     if (key0 + 16 * k >= vis) f = 1.0f, lv = 0.0f;
                 };
                 uint32_t s[64];
+                float f[4], lv[4];
+                // 64 keys and their factors
+                auto load = [&](int c) {
+                    tmem_ld32_async(t_s + c * 64, s);
+                    tmem_ld32_async(t_s + c * 64 + 32, s + 32);
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) factors(4 * c + q, f[q], lv[q]);
+                    tmem_wait(s);
+                    tmem_wait(s + 32);
+                };
                 float tm = -INFINITY;
 #pragma unroll 1
                 for (int c = 0; c < 2; ++c) {
-                    // the maximum over 64 keys (as a tree: a chain of 16 waits for
-                    // every one of them)
-                    tmem_ld32_async(t_s + c * 64, s);
-                    tmem_ld32_async(t_s + c * 64 + 32, s + 32);
-                    tmem_wait(s);
-                    tmem_wait(s + 32);
+                    load(c);
                     if (masked) {
 #pragma unroll
                         for (int e = 0; e < 64; ++e)
                             if (key0 + 64 * c + e >= vis) s[e] = 0xff800000u;
-                        // (read again below)
+                        {  // (read again below)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) tmem_st16(t_s + c * 64 + 16 * e, s + 16 * e);
-                        tmem_wait_st();
+                            for (int e = 0; e < 4; ++e) tmem_st16(t_s + c * 64 + 16 * e, s + 16 * e);
+                            tmem_wait_st();
+                        }
                     }
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
-                        float v[8], f, lv;
-#pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            v[e] = fmaxf(__uint_as_float(s[16 * q + e]), __uint_as_float(s[16 * q + 8 + e]));
-#pragma unroll
-                        for (int e = 4; e > 0; e >>= 1)
-#pragma unroll
-                            for (int z = 0; z < e; ++z) v[z] = fmaxf(v[z], v[z + e]);
-                        factors(4 * c + q, f, lv);
-                        tm = fmaxf(tm, fmaf(v[0], f, lv));
+                        const uint32_t* v = s + 16 * q;
+                        const float lo = max3(max3(v[0], v[1], v[2]), max3(v[3], v[4], v[5]), max3(v[6], v[7], v[8]));
+                        const float hi = max3(max3(v[9], v[10], v[11]), max3(v[12], v[13], v[14]), __uint_as_float(v[15]));
+                        const float top = fmaxf(lo, hi);
+                        tm = fmaxf(tm, fmaf(top, f[q], lv[q]));
                     }
                 }
                 const bool move = tm > m + kSlack;
@@ -406,27 +443,23 @@ kv8_prefill_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_const
                     }
                 }
                 const float mu = m == -INFINITY ? 0.0f : m;
-                // weights: P of 32 keys goes to the first half of their own columns
+                // weights, 64 keys at a time: P of 32 keys goes to the first half of their own
+                // columns
 #pragma unroll 1
                 for (int c = 0; c < 2; ++c) {
-                    tmem_ld32_async(t_s + c * 64, s);
-                    tmem_ld32_async(t_s + c * 64 + 32, s + 32);
-                    tmem_wait(s);
-                    tmem_wait(s + 32);
+                    load(c);
 #pragma unroll
                     for (int hf = 0; hf < 2; ++hf) {
                         uint32_t p[16];
 #pragma unroll
                         for (int q = 0; q < 2; ++q) {
-                            const int k = 4 * c + 2 * hf + q;
-                            const uint32_t* sk = s + 32 * hf + 16 * q;
-                            float f, lv;
-                            factors(k, f, lv);
-                            const uint64_t f2 = pk2(f, f), c2 = pk2(lv - mu, lv - mu);
+                            const int g = 2 * hf + q;
+                            const uint32_t* sg = s + 16 * g;
+                            const uint64_t f2 = pk2(f[g], f[g]), c2 = pk2(lv[g] - mu, lv[g] - mu);
                             uint64_t w2[8];
 #pragma unroll
                             for (int e = 0; e < 8; ++e)
-                                w2[e] = fma2(pk2(__uint_as_float(sk[2 * e]), __uint_as_float(sk[2 * e + 1])), f2, c2);
+                                w2[e] = fma2(pk2(__uint_as_float(sg[2 * e]), __uint_as_float(sg[2 * e + 1])), f2, c2);
 #pragma unroll
                             for (int e = 0; e < 8; ++e) {
                                 float p0, p1;
@@ -442,6 +475,7 @@ kv8_prefill_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_const
                                 for (int z = 0; z < e; ++z) w2[z] = add2(w2[z], w2[z + e]);
                             float a0, a1;
                             upk2(w2[0], a0, a1);
+                            const int k = 4 * c + g;
                             const float vq = __shfl_sync(0xffffffffu, my_v, k);
                             l = fmaf(a0 + a1, key0 + 16 * k < vis ? vq : 0.0f, l);
                         }
@@ -455,19 +489,15 @@ kv8_prefill_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_const
             }
             if (!ok) break;
             const float inv = (m == -INFINITY && l == 0.0f) ? 0.0f : __frcp_rn(l);
-            T* const out = y;
-            const bool write = live;
             // the next item's q is fetched while this one's last product runs
             more = take_item(it);
             if (!ok) break;
             if (more) fetch();
-            if (tiles > 0) {
-                ok = wait(o_full(x), o_phase, 0x9E2);
-                ok = __all_sync(0xffffffffu, ok);
-                if (!ok) break;
-                o_phase ^= 1u;
-                tc_fence_after();
-            }
+            ok = wait(o_full(x), o_phase, 0x9E2);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            o_phase ^= 1u;
+            tc_fence_after();
 #pragma unroll 1
             for (int c = 0; c < D / 16; ++c) {
                 uint32_t s[16];
@@ -477,19 +507,18 @@ kv8_prefill_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_const
 #pragma unroll
                     for (int e = 0; e < 16; ++e) s[e] = 0u;
                 }
-                if (write) {
+                if (live) {
+                    uint32_t p[8];
 #pragma unroll
-                    for (int q = 0; q < 2; ++q) {
-                        uint32_t p[4];
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            p[e] = (uint32_t)to16<T>(__uint_as_float(s[8 * q + 2 * e]) * inv) |
-                                   ((uint32_t)to16<T>(__uint_as_float(s[8 * q + 2 * e + 1]) * inv) << 16);
-                        *reinterpret_cast<uint4*>(out + c * 16 + 8 * q) = make_uint4(p[0], p[1], p[2], p[3]);
-                    }
+                    for (int e = 0; e < 8; ++e)
+                        p[e] = (uint32_t)to16<T>(__uint_as_float(s[2 * e]) * inv) |
+                               ((uint32_t)to16<T>(__uint_as_float(s[2 * e + 1]) * inv) << 16);
+                    *reinterpret_cast<uint4*>(y + c * 16) = make_uint4(p[0], p[1], p[2], p[3]);
+                    *reinterpret_cast<uint4*>(y + c * 16 + 8) = make_uint4(p[4], p[5], p[6], p[7]);
                 }
             }
         }
+        asm volatile("cp.async.wait_all;" ::: "memory");
     } else if (warp < 12) {
         // ------------------------------------------------------ conversion
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsConvert));
@@ -594,65 +623,70 @@ kv8_prefill_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_const
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
         int fs = 0;  // stage of the next fp16 tile in the order K0 V0 K1 V1 ...
         uint32_t fp = 0, q_phase = 0, p_phase[2] = {0, 0};
+        // descriptors of the first tiles; others differ in the address field (16-byte
+        // units, no carry: all of shared memory is 14 bits of them)
+        const uint64_t q_desc = sdesc(sbase + C::Q_OFF), k_desc = sdesc(sbase + C::F_OFF),
+                       v_desc = sdesc_mn(sbase + C::F_OFF, C::HALF);
         Item it;
 #pragma unroll 1
         while (ok && take_item(it)) {
-            if (lane == 0) {
-                const int n0 = it.tiles[0], n1 = it.tiles[1], n = max(n0, n1);
-                auto take = [&](int& stage) {  // waits for the next fp16 tile
-                    stage = fs;
-                    const bool got = wait(f_full(fs), fp, 0x9E6);
-                    if (++fs == kF16) fs = 0, fp ^= 1u;
-                    tc_fence_after();
-                    return got;
-                };
-                auto score = [&](int x, int st) {
-                    const uint32_t qa = sbase + C::Q_OFF + x * C::TILE, kb = sbase + C::F_OFF + st * C::TILE;
-#pragma unroll
-                    for (int k = 0; k < D / 16; ++k) {
-                        const uint32_t off = (k >> 2) * C::HALF + (k & 3) * 32;
-                        umma_ss(tmem + x * 128, sdesc(qa + off), sdesc(kb + off), C::IDESC_S, k != 0);
-                    }
-                    umma_commit<1>(s_full(x));
-                };
-                ok = wait(q_ready(0), q_phase, 0x9E7) &&
-                     wait(q_ready(1), q_phase, 0x9E7);
+            const int n0 = __shfl_sync(0xffffffffu, it.tiles[0], 0), n1 = __shfl_sync(0xffffffffu, it.tiles[1], 0);
+            const int n = max(n0, n1);
+            auto take = [&](int& stage) {  // waits for the next fp16 tile
+                stage = fs;
+                const bool got = __all_sync(0xffffffffu, wait(f_full(fs), fp, 0x9E6));
+                if (++fs == kF16) fs = 0, fp ^= 1u;
                 tc_fence_after();
-                int ks = 0, vs = 0;
-                // step j: the products with V of tile j (from 0), then the scores of tile j + 1
-#pragma unroll 1
-                for (int j = -1; ok && j < n; ++j) {
-                    if (j >= 0) ok = take(vs);
-                    const bool more = j + 1 < n;
-                    bool have_k = false;
-#pragma unroll 1
-                    for (int x = 0; ok && x < 2; ++x) {
-                        const int nx = x ? n1 : n0;
-                        if (j >= 0 && j < nx) {
-                            ok = wait(p_full(x), p_phase[x], 0x9E8);
-                            if (!ok) break;
-                            p_phase[x] ^= 1u;
-                            tc_fence_after();
-                            const uint32_t vb = sbase + C::F_OFF + vs * C::TILE;
+                return got;
+            };
+            auto score = [&](int x, int st) {
+                const uint64_t qa = q_desc + (uint32_t)x * (C::TILE >> 4), kb = k_desc + (uint32_t)st * (C::TILE >> 4);
 #pragma unroll
-                            for (int k = 0; k < kKeys / 16; ++k)
-                                umma_ts(tmem + C::O_COL + x * D, tmem + x * 128 + (k >> 1) * 32 + (k & 1) * 8,
-                                        sdesc_mn(vb + k * 16 * 128, C::HALF), C::IDESC_O, (j != 0 || k != 0) ? 1u : 0u);
-                            if (j + 1 == nx) umma_commit<1>(o_full(x));
-                        }
-                        if (x == 1 && j >= 0) umma_commit<1>(f_empty(vs));  // both products with V are issued
-                        if (more && !have_k) {
-                            ok = take(ks);
-                            have_k = true;
-                        }
-                        if (ok && j + 1 < nx) score(x, ks);
-                    }
-                    if (!ok) break;
-                    if (more) umma_commit<1>(f_empty(ks));
+                for (int k = 0; k < D / 16; ++k) {
+                    const uint32_t off = ((k >> 2) * C::HALF + (k & 3) * 32) >> 4;
+                    if (elect_one()) umma_ss(tmem + x * 128, qa + off, kb + off, C::IDESC_S, k != 0);
                 }
-                q_phase ^= 1u;
+                if (elect_one()) umma_commit<1>(s_full(x));
+            };
+            int ks = 0, vs = 0;
+            // step j: the products with V of tile j (from 0), then the scores of tile j + 1
+#pragma unroll 1
+            for (int j = -1; ok && j < n; ++j) {
+                if (j >= 0) ok = take(vs);
+                const bool more = j + 1 < n;
+                bool have_k = false;
+#pragma unroll 1
+                for (int x = 0; ok && x < 2; ++x) {
+                    const int nx = x ? n1 : n0;
+                    if (j >= 0 && j < nx) {
+                        ok = __all_sync(0xffffffffu, wait(p_full(x), p_phase[x], 0x9E8));
+                        if (!ok) break;
+                        p_phase[x] ^= 1u;
+                        tc_fence_after();
+                        const uint64_t vb = v_desc + (uint32_t)vs * (C::TILE >> 4);
+#pragma unroll
+                        for (int k = 0; k < kKeys / 16; ++k)
+                            if (elect_one())
+                                umma_ts(tmem + C::O_COL + x * D, tmem + x * 128 + (k >> 1) * 32 + (k & 1) * 8,
+                                        vb + (k * 16 * 128 >> 4), C::IDESC_O, (j != 0 || k != 0) ? 1u : 0u);
+                    }
+                    if (x == 1 && j >= 0 && elect_one()) umma_commit<1>(f_empty(vs));  // both products with V are issued
+                    if (more && !have_k) {
+                        ok = take(ks);
+                        have_k = true;
+                    }
+                    if (ok && j < 0) {
+                        ok = __all_sync(0xffffffffu, wait(q_ready(x), q_phase, 0x9E7));
+                        tc_fence_after();
+                    }
+                    if (ok && j + 1 < nx) score(x, ks);
+                    // (with no tile at all too: the rows' warps are never a whole item ahead)
+                    if (ok && j + 1 == nx && elect_one()) umma_commit<1>(o_full(x));
+                }
+                if (!ok) break;
+                if (more && elect_one()) umma_commit<1>(f_empty(ks));
             }
-            ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
+            q_phase ^= 1u;
         }
         if (lane == 0) {
             umma_commit<1>(drain_bar);
