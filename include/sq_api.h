@@ -473,7 +473,8 @@ SQ_API sq_status_t sq_gemm_fp4(const uint8_t* Xq, const uint8_t* Xs, const uint8
  *   kernels for few and for many rows, and any value gives a right result.
  *   T * Hq < 2^31.
  *   Workspace: SQ_OP_KV8_ATTENTION (M = T, N = Hq, K = D; the size does not depend
- *   on lengths), zeroed once before first use, as for sq_gemm_fp4.
+ *   on lengths, and is 20 MB at most for D = 128), zeroed once before first use, as
+ *   for sq_gemm_fp4.
  * ------------------------------------------------------------------------ */
 SQ_API sq_status_t sq_kv8_append(const void* Kn, const void* Vn, sq_dtype_t dt, int64_t T, int64_t Hkv, int64_t D,
                                  int64_t ldk, int64_t ldv, const int32_t* cu_q, const int32_t* seq_lens, int64_t B,

@@ -421,6 +421,45 @@ def test_prompts_of_half_a_block_of_rows():
         check_attention(batch, rows16(batch.T, 8, 64, BF, 1))
 
 
+LONG = [
+    # few rows on many keys (cut into pieces by keys): new, lens, block, Hkv, group, D
+    ([70], [6000], 16, 1, 1, 128), ([33], [9000], 64, 2, 4, 64), ([257, 3, 90], [5000, 200, 3000], 32, 2, 2, 128),
+    ([65], [1153], 16, 1, 1, 64), ([66, 1, 70] * 14, [1500, 4000, 100] * 14, 64, 3, 1, 64), ([17], [20000], 128, 8, 16, 128),
+    ([300, 2000], [8000, 2000], 16, 1, 3, 64),
+]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("new,lens,block,hkv,group,D", LONG)
+def test_prompts_on_many_keys(new, lens, block, hkv, group, D, causal):
+    """Twice the same bits, and the counters zero again."""
+    batch = ref.Batch(new, lens, hkv, D, block, seed=14)
+    dev = batch.gpu()
+    q = rows16(batch.T, hkv * group, D, BF if D == 128 else FP, 2)
+    ws = sq.workspace(sq.SQ_OP_KV8_ATTENTION, batch.T, hkv * group, D)
+    y = run_attention(batch, q, 0.09, causal, dev=dev, ws=ws, pad=8)
+    assert torch.equal(y, run_attention(batch, q, 0.09, causal, dev=dev, ws=ws))
+    check_attention(batch, q, 0.09, causal, y=y)
+    assert int(ws[256 : 256 + 4096].sum()) == 0
+
+
+@pytest.mark.gpu
+def test_prompts_on_many_keys_bad_values():
+    """In a piece of a long sequence's keys: all rows that see the block, and no row of another sequence or head."""
+    batch = ref.Batch([80, 70], [5000, 3000], 2, 128, 16, seed=15)
+    q = rows16(150, 4, 128, BF, 8)
+    clean = run_attention(batch, q, 0.1, True)
+    for name in ("kqs", "vqs"):
+        spoilt = batch.gpu()
+        spoilt[name][batch.table[0, 200], 1] = float("nan")  # positions 3200 .. 3215, head 1
+        y = run_attention(batch, q, 0.1, True, dev=spoilt)
+        bad = torch.zeros((150, 4, 128), dtype=torch.bool)
+        bad[:80, 2:] = True
+        assert torch.equal(y.isnan().cpu(), bad)
+        assert torch.equal(y[~bad.cuda()], clean[~bad.cuda()])
+
+
 @pytest.mark.gpu
 def test_attention_same_bits_every_time():
     """One workspace for batches of different lengths in turn; equal bits; the counters are zero again."""

@@ -222,6 +222,7 @@ kv8_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
     __syncthreads();
     pdl_wait();
     pdl_trigger();
+    if (blockIdx.x == 0 && threadIdx.x == 0) a.status[3] = a.cnt_bytes;
     Walk<ROWS, C::TILE> w;
     w.init(a, lane);
     int stage = 0;
@@ -674,6 +675,11 @@ size_t kv8_attention_workspace_bytes(int64_t T, int64_t Hq, int64_t D) {
         const size_t n = (size_t)attention_grid(nr) * 2 * (8 * nr) * (size_t)(D + 2) * sizeof(float);
         part = n > part ? n : part;
     }
+    // (a sequence has at most T * Hq rows of a head)
+    if (T * Hq > kRowLimit) {
+        const size_t n = kv8_prefill_part_bytes(D);
+        part = n > part ? n : part;
+    }
     return kStatusBytes + kCntBytes + part;
 }
 
@@ -726,6 +732,7 @@ extern "C" sq_status_t sq_kv8_attention(const void* Q, sq_dtype_t dt, int64_t T,
     a.causal = causal != 0;
     a.scale = scale;
     a.status = static_cast<int*>(workspace);
+    a.cnt_bytes = (int)sq::kCntBytes;
     a.cnt = reinterpret_cast<int*>(static_cast<uint8_t*>(workspace) + sq::kStatusBytes);
     a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + sq::kStatusBytes + sq::kCntBytes);
     CUtensorMap mk, mv;

@@ -46,8 +46,9 @@ struct AttnArgs {
     int64_t row_limit;  // sequences of more rows (new tokens x G) than this are the prompt kernel's
     float scale;
     int* status;
-    int* cnt;     // [grid] key tiles counted in per row tile (zero between launches)
-    float* part;  // [grid][2]: O [rows][D], m [rows], l [rows]
+    int cnt_bytes;
+    int* cnt;     // what was counted in of a row tile that several blocks share (zero between launches)
+    float* part;  // their parts: O, m and l of the rows
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -109,7 +110,9 @@ inline bool make_map_kv(CUtensorMap* m, const int8_t* base, int64_t num_blocks, 
               CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Prompts: sequences of more than kv8_row_limit rows (kv8_prefill.cu).
+// Prompts: sequences of more than kv8_row_limit rows (kv8_prefill.cu), and the
+// bytes of its parts.
+size_t kv8_prefill_part_bytes(int64_t D);
 sq_status_t launch_kv8_prefill(const char* name, sq_dtype_t dt, int64_t D, const int8_t* Kc, const int8_t* Vc,
                                const AttnArgs& a, cudaStream_t stream);
 
