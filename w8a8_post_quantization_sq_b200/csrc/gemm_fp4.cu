@@ -44,6 +44,7 @@ namespace sq {
 namespace {
 
 constexpr int BM = 128;
+constexpr int BN = 256, CG = 2;  // the pair kernel's tile: 2 x BM rows, BN columns
 constexpr int BK = 256;        // codes per stage: 128 bytes, one swizzle row
 constexpr int UMMA_K = 64;     // codes per MMA: 32 bytes
 constexpr int kEpiWarps = 8;   // two per TMEM lane quarter, each on half the tile's columns
@@ -54,7 +55,16 @@ constexpr int kStgWarpBytes = 32 * kStgRow;
 static_assert(kStgWarpBytes % 512 == 0, "staging slots must keep the 64-byte swizzle's 512-byte alignment");
 enum OutKind { kOutBF16 = 0, kOutF16 = 1, kOutF32 = 2 };
 
-template <int FMT, int BN, int CG>
+// Instruction descriptor: E2M1 operands (format 1 at bits 7 and 10), K-major,
+// N >> 3 at bit 17, scale format at bit 23 (0 E4M3, 1 E8M0), M >> 4 at bit
+// 24; which byte of a scale word to start from: bit 4 (B), bit 29 (A).
+template <int FMT>
+__device__ constexpr uint32_t idesc_fp4(int m, int n, int sf) {
+    return (1u << 7) | (1u << 10) | ((uint32_t)(n >> 3) << 17) | ((FMT == SQ_MXFP4 ? 1u : 0u) << 23) |
+           ((uint32_t)(m >> 4) << 24) | ((uint32_t)sf << 4) | ((uint32_t)sf << 29);
+}
+
+template <int FMT>
 struct Cfg {
     static constexpr int STAGES = 5;
     static constexpr int CHUNKS = FMT == SQ_NVFP4 ? 4 : 2;  // scale tiles (4 blocks) per stage and row group
@@ -81,18 +91,11 @@ struct Cfg {
     static constexpr uint32_t SB_COLS = CHUNKS * NG * 4;
     static constexpr uint32_t SET_COLS = SB_COLS + CHUNKS * 4;
     static constexpr uint32_t SF_COL = TMEM_COLS - 2 * SET_COLS;
-    static constexpr bool OVERLAP = 2 * BN > (int)SF_COL;
-    static constexpr uint32_t ACC1 = OVERLAP ? SF_COL - BN : BN;  // first column of the second accumulator
+    static constexpr uint32_t ACC1 = SF_COL - BN;  // first column of the second accumulator
     // 32-column chunks of a half accumulator that the next tile waits for
-    static constexpr int SHARED = OVERLAP ? (int)(BN - ACC1 + 31) / 32 : BN / 64;
+    static constexpr int SHARED = (int)(BN - ACC1 + 31) / 32;
     static_assert(SHARED <= BN / 64, "the shared columns lie in one half of the accumulator");
-    // Instruction descriptor: E2M1 operands (format 1 at bits 7 and 10), K-major,
-    // N >> 3 at bit 17, scale format at bit 23 (0 E4M3, 1 E8M0), M >> 4 at bit
-    // 24; which byte of a scale word to start from: bit 4 (B), bit 29 (A).
-    static constexpr uint32_t idesc(int sf) {
-        return (1u << 7) | (1u << 10) | ((uint32_t)(BN >> 3) << 17) | ((FMT == SQ_MXFP4 ? 1u : 0u) << 23) |
-               ((uint32_t)((BM * CG) >> 4) << 24) | ((uint32_t)sf << 4) | ((uint32_t)sf << 29);
-    }
+    static __device__ constexpr uint32_t idesc(int sf) { return idesc_fp4<FMT>(BM * CG, BN, sf); }
 };
 
 struct Params {
@@ -127,7 +130,7 @@ __device__ __forceinline__ int sk_owner(int x, const Params& p) {
 // A unit's work, the same sequence for all its roles: the pieces of its range
 // (the part inside one tile each; slot 0 for the first, 1 for the last, -1 where
 // a piece is a whole tile), then its whole tiles.
-template <bool SK, int CG>
+template <bool SK>
 struct Segments {
     int tile_dp, it, end;
     bool first;
@@ -168,10 +171,10 @@ __device__ __forceinline__ void tile_coords(int tile, const Params& p, int bm, i
     n0 = nb * bn;
 }
 
-template <int FMT, int CG>
+template <int FMT, int GROUP>
 __device__ __forceinline__ void umma_fp4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa, uint32_t sfb,
                                          uint32_t acc) {
-    if constexpr (FMT == SQ_NVFP4 && CG == 1)
+    if constexpr (FMT == SQ_NVFP4 && GROUP == 1)
         asm volatile(
             "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
             "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.block16 [%0], %1, %2, %3, [%5], [%6], p;\n\t}" ::"r"(d),
@@ -181,7 +184,7 @@ __device__ __forceinline__ void umma_fp4(uint32_t d, uint64_t a, uint64_t b, uin
             "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
             "tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.block16 [%0], %1, %2, %3, [%5], [%6], p;\n\t}" ::"r"(d),
             "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(sfa), "r"(sfb));
-    else if constexpr (CG == 1)
+    else if constexpr (GROUP == 1)
         asm volatile(
             "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
             "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.block32 [%0], %1, %2, %3, [%5], [%6], p;\n\t}" ::"r"(d),
@@ -326,12 +329,12 @@ __device__ __forceinline__ void epi_chunk(const Params& p, const uint32_t* r, in
     }
 }
 
-template <int FMT, int BN, int CG, int OUT, bool SK>
+template <int FMT, int OUT, bool SK>
 __global__ void __launch_bounds__(kThreads, 1)
 gemm_fp4_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ CUtensorMap tmap_b,
                 const __grid_constant__ CUtensorMap tmap_sa, const __grid_constant__ CUtensorMap tmap_sb,
                 const __grid_constant__ CUtensorMap tmap_y, const Params p) {
-    using C = Cfg<FMT, BN, CG>;
+    using C = Cfg<FMT>;
     constexpr int STAGES = C::STAGES;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -348,7 +351,7 @@ gemm_fp4_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constan
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::MISC_OFF + 4);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint32_t rank = CG == 2 ? cluster_rank() : 0u;
+    const uint32_t rank = cluster_rank();
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) {
             mbar_init(full_bar(s), 1);
@@ -366,15 +369,9 @@ gemm_fp4_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constan
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     }
     if (warp == 1) {
-        if constexpr (CG == 2) {
-            asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;"
-                         ::"r"(smem_u32(tmem_holder)), "r"(C::TMEM_COLS));
-            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
-        } else {
-            asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
-                         ::"r"(smem_u32(tmem_holder)), "r"(C::TMEM_COLS));
-            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
-        }
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;"
+                     ::"r"(smem_u32(tmem_holder)), "r"(C::TMEM_COLS));
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
     }
     if (warp == 0 && lane == 0) {
         asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmap_a)) : "memory");
@@ -385,14 +382,14 @@ gemm_fp4_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constan
     __syncwarp();
     tc_fence_before();
     __syncthreads();
-    if constexpr (CG == 2) cluster_sync_all();
+    cluster_sync_all();
     tc_fence_after();
     const uint32_t tmem_base = *tmem_holder;
     pdl_wait();
     pdl_trigger();
 
     if (SK && blockIdx.x == 0 && threadIdx.x == 0) p.status[3] = p.sk_cnt_bytes;
-    Segments<SK, CG> seg(p);
+    Segments<SK> seg(p);
     int tile, k0, k1, slot;
     if (warp == 0) {
         if (lane == 0) {
@@ -411,7 +408,7 @@ gemm_fp4_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constan
                         ok = false;
                         break;
                     }
-                    const uint32_t fb = CG == 2 ? map_to_rank(full_bar(stage), 0) : full_bar(stage);
+                    const uint32_t fb = map_to_rank(full_bar(stage), 0);
                     if (rank == 0) mbar_expect_tx(full_bar(stage), CG * (C::A_BYTES + C::B_BYTES));
                     mbar_expect_tx(sfull_bar(stage), C::SA_BYTES + C::SB_BYTES);
                     tma_load_3d<CG>(sbase + C::A_OFF + stage * C::A_BYTES, &tmap_a, fb, kb * (BK / 2), m0, 0);
@@ -441,10 +438,9 @@ gemm_fp4_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constan
             bool ok = true;
             for (; ok && seg.next(p, tile, k0, k1, slot); ++local) {
                 const int acc = local & 1;
-                // accumulators that share columns: the previous tile's shared
-                // columns (and all of the tile before it) have been read; else
-                // all of the tile before the previous one
-                const int prev = C::OVERLAP ? local - 1 : local - 2;
+                // the previous tile's shared columns (and all of the tile before it)
+                // have been read
+                const int prev = local - 1;
                 if (prev >= 0 &&
                     !wait_fast(tempty_bar(prev & 1), (uint32_t)(prev >> 1) & 1u, abort_flag, p.status, 0x8E2)) {
                     ok = false;
@@ -514,10 +510,7 @@ gemm_fp4_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constan
                 asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) {
-                    if constexpr (CG == 2) mbar_arrive_remote(map_to_rank(sready_bar(stage), 0));
-                    else mbar_arrive(sready_bar(stage));
-                }
+                if (lane == 0) mbar_arrive_remote(map_to_rank(sready_bar(stage), 0));
                 set ^= 1u;
                 if (++before == STAGES) before = 0, before_phase ^= 1u;
                 if (++stage == STAGES) stage = 0, phase ^= 1u;
@@ -534,10 +527,7 @@ gemm_fp4_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constan
         auto release_acc = [&](int a) {
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) {
-                if constexpr (CG == 2) mbar_arrive_remote(map_to_rank(tempty_bar(a), 0));
-                else mbar_arrive(tempty_bar(a));
-            }
+            if (lane == 0) mbar_arrive_remote(map_to_rank(tempty_bar(a), 0));
         };
         int local = 0;
         for (; seg.next(p, tile, k0, k1, slot); ++local) {
@@ -570,7 +560,7 @@ gemm_fp4_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constan
             const int acc = local & 1;
             // a warp that reads no shared column hands the buffer back at once
             // (the tile before this one is read in full by now)
-            const bool shares = !C::OVERLAP || half == 1 - acc;
+            const bool shares = half == 1 - acc;
             if (!shares) release_acc(acc);
             const bool ok = wait_fast(tfull_bar(acc), (uint32_t)(local >> 1) & 1u, abort_flag, p.status, 0x8E4);
             if (!__all_sync(0xffffffffu, ok)) break;
@@ -581,7 +571,7 @@ gemm_fp4_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constan
             uint32_t r[32];
             // shared columns first: the upper half's last chunks of the first
             // accumulator, the lower half's first ones of the second
-            const int turn = C::OVERLAP && acc == 0 && half == 1 ? NCH - C::SHARED : 0;
+            const int turn = acc == 0 && half == 1 ? NCH - C::SHARED : 0;
             if constexpr (SK) {
                 if (slot >= 0) {
                     // a piece: park the sums; the one that completes the tile's
@@ -651,13 +641,10 @@ gemm_fp4_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constan
     __syncwarp();
     tc_fence_before();
     __syncthreads();
-    if constexpr (CG == 2) cluster_sync_all();
+    cluster_sync_all();
     if (warp == 1) {
         tc_fence_after();
-        if constexpr (CG == 2)
-            asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(C::TMEM_COLS));
-        else
-            asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(C::TMEM_COLS));
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(C::TMEM_COLS));
     }
 }
 
@@ -689,7 +676,7 @@ struct SCfg {
     static constexpr uint32_t SET_COLS = 2 * CHUNKS * 4;
     static constexpr uint32_t SF_COL = 128, TMEM_COLS = 256;
     static_assert(SF_COL + 2 * SET_COLS <= TMEM_COLS, "tensor memory");
-    static constexpr uint32_t idesc(int sf) { return Cfg<FMT, 128, 1>::idesc(sf); }
+    static constexpr uint32_t idesc(int sf) { return idesc_fp4<FMT>(BM, 128, sf); }
 };
 constexpr int kSplitThreads = 6 * 32;
 
@@ -1005,8 +992,7 @@ sq_status_t map_failed(const char* name) {
 
 template <int FMT, int OUT>
 sq_status_t launch_pairs(const char* name, const Call& c, const Plan& pl, Params& p, cudaStream_t stream) {
-    constexpr int BN = 256, CG = 2;
-    using C = Cfg<FMT, BN, CG>;
+    using C = Cfg<FMT>;
     const int64_t tk = fp4_tiles_k(FMT, c.K);
     CUtensorMap ta, tb, tsa, tsb, ty;
     memset(&ty, 0, sizeof(ty));
@@ -1022,7 +1008,7 @@ sq_status_t launch_pairs(const char* name, const Call& c, const Plan& pl, Params
     const int64_t per = (int64_t)BM * CG * c.K / 2;
     const int64_t g = (48ll << 20) / per;
     p.group_m = (int)(g < 1 ? 1 : g > p.num_m ? p.num_m : g);
-    auto fn = p.sk_tiles > 0 ? gemm_fp4_kernel<FMT, BN, CG, OUT, true> : gemm_fp4_kernel<FMT, BN, CG, OUT, false>;
+    auto fn = p.sk_tiles > 0 ? gemm_fp4_kernel<FMT, OUT, true> : gemm_fp4_kernel<FMT, OUT, false>;
     if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM_ALLOC) != cudaSuccess)
         return check_launch(name);
     launch_pdl_cluster(fn, dim3(pl.grid), dim3(kThreads), C::SMEM_ALLOC, stream, 2, ta, tb, tsa, tsb, ty, p);
