@@ -222,7 +222,6 @@ kv8_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
     __syncthreads();
     pdl_wait();
     pdl_trigger();
-    if (blockIdx.x == 0 && threadIdx.x == 0) a.status[3] = a.cnt_bytes;
     Walk<ROWS, C::TILE> w;
     w.init(a, lane);
     int stage = 0;

@@ -358,7 +358,6 @@ kv8_prefill_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_const
     const uint32_t tmem = *tmem_holder;
     pdl_wait();
     pdl_trigger();
-    if (blockIdx.x == 0 && threadIdx.x == 0) a.status[3] = a.cnt_bytes;
     auto wait = [&](uint32_t bar, uint32_t parity, int code) {
         return wait_suspended(bar, parity, abort_flag, a.status, code, kTimeoutNs);
     };
@@ -883,6 +882,8 @@ kv8_prefill_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_const
             }
         }
     }
+    // pieces that gave up leave their rows counted in: what is to be cleared with the status
+    if (SPLIT && !ok) a.status[3] = a.cnt_bytes;
     __syncwarp();
     tc_fence_before();
     __syncthreads();

@@ -46,7 +46,7 @@ struct AttnArgs {
     int64_t row_limit;  // sequences of more rows (new tokens x G) than this are the prompt kernel's
     float scale;
     int* status;
-    int cnt_bytes;
+    int cnt_bytes;  // of the counters
     int* cnt;     // what was counted in of a row tile that several blocks share (zero between launches)
     float* part;  // their parts: O, m and l of the rows
 };
