@@ -31,6 +31,8 @@
 //     cluster, which adds them up through its shared memory, in part order.
 //     (Parked in global memory and counted by atomics, the parts cost 2.5 us
 //     more: 16 x 4096 x 4096 9.9 us, so 6.2 us.)
+// What bounds it: the operands' way from L2 (11.6 TB/s) and power at 4096 x 12288 x
+// 12288 (253-270 us, 4.6-4.9 PFLOP/s), HBM and latency for few rows.
 // Every wait is bounded (about 2 s), code 0x8E1 + role in the status word.
 #include <cstring>
 #include <type_traits>

@@ -32,6 +32,8 @@
 // bytes and by the conversions, so the products are mma.m16n8k16 with the keys
 // (K) and the columns (V) on the 16-wide side and 8 rows on the other: half the
 // instructions and registers of the usual orientation.
+// Measured (32 heads over 8, D 128): 64 sequences of up to 8192 keys 106 us, 5.5 TB/s
+// (0.84 of the copy rate); one of 1000 keys 10.5 us, the chain of loads and the join.
 #include <cstring>
 
 #include "sq_internal.h"
