@@ -514,11 +514,10 @@ kv8_prefill_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_const
 #pragma unroll
                         for (int e = 0; e < 64; ++e)
                             if (key0 + 64 * c + e >= vis) s[e] = 0xff800000u;
-                        {  // (read again below)
+                        // (read again below)
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) tmem_st16(t_s + c * 64 + 16 * e, s + 16 * e);
-                            tmem_wait_st();
-                        }
+                        for (int e = 0; e < 4; ++e) tmem_st16(t_s + c * 64 + 16 * e, s + 16 * e);
+                        tmem_wait_st();
                     }
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
