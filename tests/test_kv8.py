@@ -514,3 +514,42 @@ def test_append_then_attend_in_a_graph():
         batch.lens = [n + 1 for n in batch.lens]
         dev["lens"] += 1
     sq.sq_workspace_status(ws)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("new,lens", [([70, 130, 1], [75, 200, 9]), ([70, 3], [3000, 40])])
+@pytest.mark.parametrize("kind", ["zeros", "zero_block", "tiny_keys", "zero_scale"])
+def test_prompt_of_equal_scores(kind, new, lens, D, causal):
+    """Rows whose scores are all equal because q, K or the scale is zero: equal weights. The blocks of zero (or
+    1e-7 sized) keys have the largest scales that there are, and rows end inside a block; whole and cut by keys."""
+    batch = ref.Batch(new, lens, 2, D, 16, seed=21)
+    dev = batch.gpu()
+    q = rows16(batch.T, 4, D, BF, 1)
+    k, v = rows16(batch.T, 2, D, BF, 2), rows16(batch.T, 2, D, BF, 3)
+    if kind == "zeros":
+        q, k, v = (torch.zeros_like(x) for x in (q, k, v))
+    elif kind == "tiny_keys":
+        q, k = torch.zeros_like(q), k * 1e-7
+    else:
+        k[19:60] = 0  # a whole block of the first sequence and more
+        if kind == "zero_block":
+            q = torch.zeros_like(q)
+    check_append(batch, k, v, dev)
+    check_attention(batch, q, 0.0 if kind == "zero_scale" else None, causal, dev=dev)
+
+
+@pytest.mark.gpu
+def test_prompt_of_zeros_with_bad_scales():
+    """A NaN scale of a block reaches the zero rows that see it, and a NaN score scale every row that sees a key."""
+    batch = ref.Batch([80, 90], [80, 2000], 1, 64, 16, seed=22)
+    q = torch.zeros((170, 2, 64), dtype=BF)
+    for name in ("kqs", "vqs"):
+        spoilt = batch.gpu()
+        spoilt[name][batch.table[0, 2]] = float("nan")  # positions 32 .. 47
+        y = run_attention(batch, q, 0.1, True, dev=spoilt)
+        bad = torch.zeros((170, 2, 64), dtype=torch.bool)
+        bad[32:80] = True
+        assert torch.equal(y.isnan().cpu(), bad)
+    assert bool(run_attention(batch, rows16(170, 2, 64, BF, 1), float("nan"), True).isnan().all())

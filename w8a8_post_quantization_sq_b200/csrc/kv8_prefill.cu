@@ -127,6 +127,12 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 __device__ __forceinline__ float max3(uint32_t a, uint32_t b, uint32_t c) {
     return max3(__uint_as_float(a), __uint_as_float(b), __uint_as_float(c));
 }
+// The larger one, NaN if either is (fmaxf drops NaN).
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float y;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+    return y;
+}
 // 16 bytes to shared memory (zeros without `live`), not waited for.
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool live) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
@@ -449,8 +455,7 @@ kv8_prefill_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_const
                 unpack<T>(make_uint4(max(m2 & 0xffffu, m2 >> 16), 0, 0, 0), top);
                 const uint32_t field = min(max(__float_as_uint(top[0]) >> 23, 1u), 253u);
                 const float down = copysignf(__uint_as_float((254u - field) << 23), a.scale);
-                // (never 0: a masked score is -inf before it is multiplied)
-                crow = fmaxf(fabsf(a.scale) * kLog2e * __uint_as_float(field << 23), 1.17549435e-38f);
+                crow = fabsf(a.scale) * kLog2e * __uint_as_float(field << 23);
 #pragma unroll 4
                 for (int e = 0; e < D / 8; ++e) {
                     uint4* at = reinterpret_cast<uint4*>(smem + C::Q_OFF + x * C::TILE + unit_of(row, e));
@@ -489,9 +494,12 @@ kv8_prefill_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_const
                 const int key0 = (it.k0 + j) * kKeys;
                 const bool masked = __any_sync(0xffffffffu, key0 + kKeys > vis);
                 // per 16 keys: score factor and -log2 of the V scale; of keys that
-                // this row does not see nothing is taken, whatever their scales
+                // this row does not see nothing is taken, whatever their scales.
+                // The factor is never 0 (a row of zeros times a block of zeros, whose
+                // 1 / kqs is 8e-11, would be): masked scores are -inf before they
+                // are multiplied, and -inf x 0 is NaN. A NaN scale stays NaN.
                 auto factors = [&](int k, float& f, float& lv) {
-                    f = crow * __shfl_sync(0xffffffffu, my_k, k);
+                    f = max_nan(crow * __shfl_sync(0xffffffffu, my_k, k), 1.17549435e-38f);
                     lv = __shfl_sync(0xffffffffu, my_lv, k);
                     if (key0 + 16 * k >= vis) f = 1.0f, lv = 0.0f;
                 };
