@@ -423,3 +423,24 @@ def test_no_rows():
     sq.sq_quantize_act_fp4(torch.empty((0, 64), device="cuda"), None, 0, True, None, e(0, 32), e(0), torch.empty(0).cuda())
     sq.sq_gemm_fp4(e(0, 32), e(0), wq, wsc, 0, None, qw, None, torch.empty((0, 8), device="cuda"),
                    sq.workspace(sq.SQ_OP_GEMM_FP4, 0, 8, 64))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dt", DTYPES)
+@pytest.mark.parametrize("smooth", [False, True])
+def test_quantise_static_past_the_largest(dt, smooth):
+    """A static scale under which finite values pass fp32's largest: they saturate, and so does their block's scale."""
+    static = float(np.float32(1e36 if dt == torch.float16 else 1e30))
+    x = data(8, 256, torch.float32)
+    top = torch.finfo(dt).max / (4 if smooth else 1)  # (the quotient by s is still finite)
+    x[0] = top
+    x[1, 5] = -top
+    x[2, ::7] = top
+    x[3] *= 1e-3 if dt == torch.float16 else 1e-27
+    x[3, ::16] = -top  # beside values of a few hundred times the largest code
+    x[4, 9] = float("inf")
+    x[5, 40] = float("nan")
+    x[6] = 0
+    x[6, 100] = top
+    s = torch.rand(256, generator=torch.Generator().manual_seed(3)) + 0.5 if smooth else None
+    check_quant(x.to(dt), sq.SQ_NVFP4, s, static=static)

@@ -29,6 +29,7 @@ namespace {
 
 enum Smooth { kNone = 0, kMul = 1, kDiv = 2 };
 constexpr uint32_t kInfBits = 0x7f800000u;
+constexpr float kMaxF32 = 0x1.fffffep+127f;
 
 // 32 bytes a lane: a warp's access then covers whole 32-byte sectors, which two
 // accesses of 16 bytes touch twice (4096 x 12288: dequantisation 29.7 -> 25.5 us,
@@ -200,7 +201,9 @@ __device__ __forceinline__ void emit_unit(const QuantArgs& a, uint8_t* codes, ui
     uint32_t byte;
     uint2 w;
     if constexpr (FMT == SQ_NVFP4) {
-        const float top = __fmul_rn(__uint_as_float(bits), qs);
+        // (a given scale may carry finite values past fp32's largest: held there,
+        // they saturate below, where an infinity would make NaN of the residuals)
+        const float top = fminf(__fmul_rn(__uint_as_float(bits), qs), kMaxF32);
         // fl(top / 6), the quotient rounded as in codes8
         float sixth = __fmul_rn(top, 0x1.555556p-3f);
         sixth = __fmaf_rn(__fmaf_rn(sixth, -6.0f, top), 0x1.555556p-3f, sixth);
@@ -212,7 +215,11 @@ __device__ __forceinline__ void emit_unit(const QuantArgs& a, uint8_t* codes, ui
         if (a.static_qs) {
             const uint64_t qs2 = pk2(qs, qs);
 #pragma unroll
-            for (int e = 0; e < 16; e += 2) upk2(mul2(pk2(v[e], v[e + 1]), qs2), v[e], v[e + 1]);
+            for (int e = 0; e < 16; e += 2) {
+                upk2(mul2(pk2(v[e], v[e + 1]), qs2), v[e], v[e + 1]);
+                v[e] = fminf(fmaxf(v[e], -kMaxF32), kMaxF32);
+                v[e + 1] = fminf(fmaxf(v[e + 1], -kMaxF32), kMaxF32);
+            }
         } else {
             // qs is a power of two: u / b is v / (b / qs), with the same bits
             inv = __fmul_rn(inv, qs);
