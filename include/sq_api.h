@@ -467,8 +467,12 @@ SQ_API sq_status_t sq_gemm_fp4(const uint8_t* Xq, const uint8_t* Xs, const uint8
  *   is zero. A block number outside the cache makes the rows that would read it
  *   NaN. Tokens behind cu_q[B] are left as they were.
  *   Q, Y: [T, Hq, D] of dt in {F16, BF16}, token strides ldq, ldy (multiples of
- *   8), 16-byte aligned. Scores, maxima, sums and outputs are fp32; the softmax
- *   weights are rounded to fp16 (2^-11) for the second product.
+ *   8), 16-byte aligned. Scores, maxima, sums and outputs are fp32. For the two
+ *   products, q becomes fp16 after a power of two has brought the row's largest
+ *   into [1, 2) (exact, but for elements below 2^-14, which are off by 2^-25 at
+ *   most), and the weights over vqs are rounded to fp16 (2^-11 relative down to
+ *   2^-21 of the row's largest, 2^-32 of the largest below that); the weights' sum
+ *   is not.
  *   max_q: the largest number of new tokens of a sequence; it chooses between the
  *   kernels for few and for many rows, and any value gives a right result.
  *   T * Hq < 2^31.

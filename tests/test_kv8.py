@@ -553,3 +553,37 @@ def test_prompt_of_zeros_with_bad_scales():
         bad[32:80] = True
         assert torch.equal(y.isnan().cpu(), bad)
     assert bool(run_attention(batch, rows16(170, 2, 64, BF, 1), float("nan"), True).isnan().all())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("new", [1, 5, 70])
+def test_attention_one_high_score_before_a_long_tail(new, D):
+    """A first key whose weight is 2^26 times each other's and whose value is zero, so the output is the tail's alone;
+    heads enough that nobody's keys are cut into parts (which have maxima of their own). A weight below 2^-21 of the
+    largest is an fp16 subnormal once it is lifted by 2^7: off by 2^-25 2^-7 of the largest at most (all values have one
+    scale here), in all 2^-32 sum |v|, beside what check_attention counts."""
+    B, H, N = 64, 8, 2005
+    batch = ref.Batch([new] * B, [N] * B, H, D, 128, seed=23)
+    batch.table[:] = batch.table[0]  # all sequences read the same blocks
+    batch.k[:] = 0
+    batch.kqs[:] = 127.0
+    batch.vqs[:] = 31.75
+    batch.v = np.maximum(np.abs(batch.v), 1)  # nothing cancels
+    first = batch.table[0, 0]
+    batch.k[first, :, 0, 0] = 127
+    batch.v[first, :, 0] = 0
+    q = torch.zeros((batch.T, 2 * H, D), dtype=BF)
+    q[:, :, 0] = 18.0  # 25.97 in log2
+    y = run_attention(batch, q, 1.0, False).double()
+    one = ref.Batch([new], [N], H, D, 128)
+    for name in ("k", "v", "kqs", "vqs"):
+        setattr(one, name, getattr(batch, name))
+    one.table = batch.table[:1]
+    want, mass = ref.attention(one, q[:new].double().cuda(), 1.0, False)
+    used = batch.v[batch.table[0]].transpose(1, 0, 2, 3).reshape(H, -1, D)[:, :N].astype(np.float64).sum(1)
+    floor = torch.from_numpy(2.0**-32 * used / 31.75).cuda().repeat_interleave(2, 0)
+    tol = 2.0**-8 * want + 3.1e-3 * mass + floor
+    assert bool((want > 50 * floor).all())
+    err = (y.view(B, new, 2 * H, D) - want).abs()
+    assert bool((err <= tol).all()), float((err / tol).max())

@@ -8,17 +8,18 @@
 // The codes go through the tensor cores as fp16, which holds every int8
 // exactly; the two scales of a block multiply the 16 x 16 score tiles in fp32:
 // the K scale multiplies the scores, and the V scale is folded into the
-// softmax's exponent. With t_j = log2(e) s_j - log2(vqs(j)) and a running
-// maximum m of t (not of s),
+// softmax's exponent. With t_j = log2(e) s_j - log2(vqs(j)) and m, the running
+// maximum of t (not of s) less 7,
 //   P_j = 2^(t_j - m),  O = sum_j P_j V_j,  l = sum_j P_j vqs(j),  o = O / l,
-// so P, the only quantity rounded to fp16, stays below 2^8 whatever the scales,
-// and V is never scaled. P's rounding is at most 2^-11 relative, as that of an
-// fp16 output; m, l, O are fp32. The running maximum is moved only when a
-// score passes it by more than 2^8 (the rescaling of O then costs nothing on
-// most tiles; P <= 256 is far inside fp16).
-// q is scaled by a power of two per row to [1, 2) before it becomes fp16, so a
-// bf16 q keeps its 8 bits (elements 2^14 times smaller than the row's largest
-// lose bits that the fp32 sum could not hold either).
+// and V is never scaled. m is moved only when a t passes it by 15 (the rescaling
+// of O then costs nothing on most tiles), so P, the only quantity rounded to
+// fp16, stays below 2^15 whatever the scales. Its rounding is at most 2^-11
+// relative, as that of an fp16 output, down to 2^-21 of the largest P of the keys
+// that share m; below that it is an fp16 subnormal, off by 2^-32 of the largest.
+// m, l, O are fp32.
+// q is scaled by a power of two per row to [1, 2) before it becomes fp16, so it
+// keeps its bits, but for elements that are then below 2^-14 (fp16 subnormals,
+// off by 2^-25 at most).
 //
 // Work: rows (new token, query head of the group) of one sequence and K/V head
 // make row tiles of 8 or 16; the keys of each row tile are cut into tiles of 64 (128),
@@ -419,7 +420,7 @@ kv8_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
                         }
                         q = fmaxf(q, __shfl_xor_sync(0xffffffffu, q, 4));
                         q = fmaxf(q, __shfl_xor_sync(0xffffffffu, q, 8));
-                        tm[z][x] = fmaxf(q, __shfl_xor_sync(0xffffffffu, q, 16));
+                        tm[z][x] = fmaxf(q, __shfl_xor_sync(0xffffffffu, q, 16)) - kLift;
                         move |= tm[z][x] > m[z][x] + kSlack;
                     }
                 if (__any_sync(0xffffffffu, move)) {

@@ -3,7 +3,7 @@
 //
 // The same formula, scales and rounding as for single tokens (kv8_attention.cu):
 // int8 codes as fp16, the K scale on the fp32 scores, the V scale in the
-// softmax's exponent, P in fp16 below 2^8, a running maximum that moves only
+// softmax's exponent, P in fp16 below 2^15, a running maximum that moves only
 // when a score passes it by 2^8. Here both products run on tcgen05 (kind::f16):
 //   S = Q K^T   128 rows x 128 keys, both from shared memory
 //   O += P V    P from tensor memory (it overwrites half of S), V from shared
@@ -536,6 +536,7 @@ kv8_prefill_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_const
                         tm = fmaxf(tm, fmaf(top, f[q], lv[q]));
                     }
                 }
+                tm -= kLift;
                 const bool move = tm > m + kSlack;
                 if (__any_sync(0xffffffffu, move)) {
                     const float to = move ? tm : m;

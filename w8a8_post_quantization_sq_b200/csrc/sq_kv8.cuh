@@ -30,8 +30,11 @@ sq_status_t check_kv8(const char* name, int64_t T, int64_t B, int64_t Hkv, int64
 
 // ---------------------------------------------------------------- attention
 constexpr float kLog2e = 1.4426950408889634f;
-// The running maximum follows a score only when that is this far (in log2) above it.
-constexpr float kSlack = 8.0f;
+// The running maximum follows a score only when that is this far (in log2) above it,
+// and is kept this far below the score that it then follows: the weights stay below
+// 2^(kSlack + kLift), inside fp16, and those down to 2^-21 of the largest are normal
+// fp16 numbers, smaller ones off by 2^-32 of the largest at most.
+constexpr float kSlack = 8.0f, kLift = 7.0f;
 
 struct AttnArgs {
     const void* Q;
