@@ -436,12 +436,13 @@ void launch_quant(const QuantArgs& a, cudaStream_t stream) {
         else if (upt == 2) launch_quant_upt<T, FMT, SM, 2, 256>(a, tl, stream);
         else if (upt == 3) launch_quant_upt<T, FMT, SM, 3, 256>(a, tl, stream);
         else launch_quant_upt<T, FMT, SM, 4, 256>(a, tl, stream);
-    } else {
-        if (upt <= 3) launch_quant_upt<T, FMT, SM, 3, 512>(a, tl, stream);
-        else if (upt == 4) launch_quant_upt<T, FMT, SM, 4, 512>(a, tl, stream);
-        else if (upt <= 6 && Unit<T, SM>::RAW) launch_quant_upt<T, FMT, SM, 6, 512>(a, tl, stream);
-        else launch_quant_upt<T, FMT, SM, 0, 512>(a, tl, stream);
+        return;
     }
+    if (upt <= 3) return launch_quant_upt<T, FMT, SM, 3, 512>(a, tl, stream);
+    if (upt == 4) return launch_quant_upt<T, FMT, SM, 4, 512>(a, tl, stream);
+    if constexpr (Unit<T, SM>::RAW)  // (others do not fit a thread's registers)
+        if (upt <= 6) return launch_quant_upt<T, FMT, SM, 6, 512>(a, tl, stream);
+    launch_quant_upt<T, FMT, SM, 0, 512>(a, tl, stream);
 }
 
 template <typename T, int FMT>
