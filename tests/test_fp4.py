@@ -444,3 +444,39 @@ def test_quantise_static_past_the_largest(dt, smooth):
     x[6, 100] = top
     s = torch.rand(256, generator=torch.Generator().manual_seed(3)) + 0.5 if smooth else None
     check_quant(x.to(dt), sq.SQ_NVFP4, s, static=static)
+
+
+def exact_operand(rows, K, fmt, seed):
+    """Any codes, block scales 1, 2 and 4, row scales powers of two: products are multiples of 1/4."""
+    g = np.random.default_rng(seed)
+    codes = g.integers(0, 16, (rows, K), dtype=np.uint8)
+    step = g.integers(0, 3, (rows, K // ref.BLOCK[fmt]))
+    byte = (0x38 + 8 * step if fmt == 0 else 127 + step).astype(np.uint8)
+    q = 2.0 ** g.integers(-3, 4, rows) if fmt == 0 else None
+    dev = (torch.from_numpy(ref.pack(codes)).cuda(), torch.from_numpy(ref.tile(byte)).cuda(),
+           None if q is None else torch.from_numpy(q).float().cuda())
+    v = torch.tensor(ref.GRID, device="cuda")[torch.from_numpy(codes & 7).cuda().int()]
+    v = torch.where(torch.from_numpy(codes & 8).cuda() > 0, -v, v)
+    v *= torch.from_numpy(2.0**step).cuda().repeat_interleave(ref.BLOCK[fmt], 1)
+    return dev, v, q
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("M,N,K", [(1, 1024, 8192), (16, 4096, 4096), (64, 384, 2080), (333, 1001, 1056), (2100, 2344, 1120),
+                                   (2560, 2560, 12288), (2500, 2490, 12320), (1024, 7168, 16384)])
+def test_gemm_exact(M, N, K, fmt):
+    """Sums that fp32 holds exactly in any order (multiples of 1/4 whose absolute sum stays below 2^22, 24 bits): the
+    product to the last bit, in parts of a k-loop, whole tiles and the last wave's pieces."""
+    (xq, xs, qx), xv, rx = exact_operand(M, K, fmt, 1)
+    (wq, wsc, qw), wv, rw = exact_operand(N, K, fmt, 2)
+    assert float((xv.abs() @ wv.abs().T).max()) < 2.0**22
+    want = xv @ wv.T
+    if fmt == 0:
+        want = want / torch.from_numpy(rx).cuda()[:, None] / torch.from_numpy(rw).cuda()
+    ws = sq.workspace(sq.SQ_OP_GEMM_FP4, M, N, K)
+    for dt in (torch.float32, torch.bfloat16):
+        y = torch.empty((M, N), dtype=dt, device="cuda")
+        sq.sq_gemm_fp4(xq, xs, wq, wsc, fmt, qx, qw, None, y, ws)
+        assert torch.equal(y, want.float().to(dt))
+    sq.sq_workspace_status(ws)
