@@ -480,3 +480,10 @@ def test_gemm_exact(M, N, K, fmt):
         sq.sq_gemm_fp4(xq, xs, wq, wsc, fmt, qx, qw, None, y, ws)
         assert torch.equal(y, want.float().to(dt))
     sq.sq_workspace_status(ws)
+
+
+def test_refuses_an_unaligned_workspace(L):
+    """Its counters and sums are accessed up to 16 bytes at a time: host error, no launch."""
+    p, odd = ctypes.c_void_p(1 << 20), ctypes.c_void_p((1 << 20) + 8)
+    status = L.sq_gemm_fp4(p, p, p, p, 0, 16, 16, 32, p, 1, p, 1, None, 2, p, 16, odd, 256, None)
+    assert status == 3 and "workspace must be 16-byte aligned" in L.sq_last_error_string().decode()

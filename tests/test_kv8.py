@@ -587,3 +587,11 @@ def test_attention_one_high_score_before_a_long_tail(new, D):
     assert bool((want > 50 * floor).all())
     err = (y.view(B, new, 2 * H, D) - want).abs()
     assert bool((err <= tol).all()), float((err / tol).max())
+
+
+def test_refuses_an_unaligned_workspace(L):
+    """Its counters and sums are accessed up to 16 bytes at a time: host error, no launch."""
+    p, odd = ctypes.c_void_p(1 << 20), ctypes.c_void_p((1 << 20) + 8)
+    status = L.sq_kv8_attention(p, 2, 4, 8, 2, 64, 512, p, p, p, p, 8, 16, p, p, 1, p, 4, 4, 0.125, 1, 4, p, 512, odd,
+                                1 << 24, None)
+    assert status == 3 and "workspace must be 16-byte aligned" in L.sq_last_error_string().decode()

@@ -1080,6 +1080,7 @@ extern "C" sq_status_t sq_gemm_fp4(const uint8_t* Xq, const uint8_t* Xs, const u
                "%s: codes and block scales must be 16-byte aligned", name);
     SQ_REQUIRE(workspace && ws_bytes >= sq::kStatusBytes, SQ_ERR_INVALID_ARG, "%s: needs a workspace of %zu bytes", name,
                sq::kStatusBytes);
+    SQ_REQUIRE(sq::aligned16(workspace), SQ_ERR_ALIGNMENT, "%s: the workspace must be 16-byte aligned", name);
     const sq::Plan pl = sq::plan_fp4(M, N, K);
     const int eb = sq::dtype_bytes(out_dt);
     sq::Params p;

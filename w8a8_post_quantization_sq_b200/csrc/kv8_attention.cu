@@ -710,6 +710,7 @@ extern "C" sq_status_t sq_kv8_attention(const void* Q, sq_dtype_t dt, int64_t T,
                SQ_ERR_ALIGNMENT, "%s: Q, Y, the caches and token strides must be 16-byte aligned", name);
     SQ_REQUIRE(workspace && ws_bytes >= sq::kv8_attention_workspace_bytes(T, Hq, D), SQ_ERR_INVALID_ARG,
                "%s: needs a workspace of %zu bytes", name, sq::kv8_attention_workspace_bytes(T, Hq, D));
+    SQ_REQUIRE(sq::aligned16(workspace), SQ_ERR_ALIGNMENT, "%s: the workspace must be 16-byte aligned", name);
     sq::AttnArgs a;
     memset(&a, 0, sizeof(a));
     a.Q = Q;
