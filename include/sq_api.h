@@ -423,7 +423,8 @@ SQ_API sq_status_t sq_gemm_fp8(const uint8_t* Xq, const uint8_t* Wq, int64_t M, 
  *   idle, arrival counters (at the same bytes for every shape, zero again after
  *   every completed call) and the parked sums of that wave's split k-loops. A
  *   smaller one (at least 256 bytes) is accepted and splits nothing. Calls sharing
- *   one must not run concurrently.
+ *   one must not run concurrently, and calls of other operations need one of their
+ *   own (their counters and sums lie elsewhere).
  * ------------------------------------------------------------------------ */
 SQ_API size_t sq_fp4_scale_bytes(sq_fp4_t fmt, int64_t rows, int64_t K);
 SQ_API sq_status_t sq_quantize_weight_fp4(const void* W, sq_dtype_t dt, int64_t N, int64_t K, const float* s,

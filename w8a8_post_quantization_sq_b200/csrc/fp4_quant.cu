@@ -17,8 +17,12 @@
 // inputs as they came (held as fp32, three units took 109 registers and two
 // blocks per SM: 4096 x 12288 bf16 65 us). Rows too wide for that (over 32768
 // elements; 49152 of 16 bits) are read twice, the second time from L2.
-// What bounds it: the bytes (2 in and 0.56 out per 16-bit element; 4096 x 12288
-// bf16 to NVFP4 50 us, 4.6 TB/s of 6.5), for few rows the launch (16 x 4096: 4.2 us).
+// What bounds it, at 4096 x 12288 (us, of them the bytes at 6.54 TB/s): quantisation
+// the bytes and the codes' arithmetic between them, bf16 to NVFP4 26.8 (19.7), to MXFP4
+// 21.4 (19.5), fp32 44.8 (35.1) and 34.4 (34.9); with a smoothing scale the fp32
+// values held and, for activations, a division each (bf16 to NVFP4 80.4 with 1 / s, 57.8
+// with s; to MXFP4 54.1 and 39.5). Dequantisation to bf16 24.2 (19.7). Few rows: the
+// launch and one chain of loads (16 x 4096: 2.9 and 1.6).
 #include <cuda_fp8.h>
 
 #include "sq_common.cuh"

@@ -31,8 +31,14 @@
 //     cluster, which adds them up through its shared memory, in part order.
 //     (Parked in global memory and counted by atomics, the parts cost 2.5 us
 //     more: 16 x 4096 x 4096 9.9 us, so 6.2 us.)
-// What bounds it: the operands' way from L2 (11.6 TB/s) and power at 4096 x 12288 x
-// 12288 (253-270 us, 4.6-4.9 PFLOP/s), HBM and latency for few rows.
+// What bounds it at 4096 x 12288 x 12288 (NVFP4 253-280 us over boxes and ten calls in
+// a row, 4.4-4.9 PFLOP/s): called without end, the power cap (990 W, the SM clock at
+// 1.59 of 1.965 GHz, 311 us). In short runs the tensor cores are active 55 % of the
+// cycles and nothing that was measured is full: L2 delivers 11.4 TB/s, where the
+// int8 pair kernel takes 12.0 with its tensor cores active 89 %; and MXFP4, with half
+// the scale bytes, is no faster (250-268 us). The scales' way to tensor memory starts
+// only when the MMAs of two stages before are complete. Few rows: the weight's bytes
+// and latency (16 x 12288 x 12288 18.4 us, 13.1 of bytes; 16 x 16384 x 4096 9.4, 5.9).
 // Every wait is bounded (about 2 s), code 0x8E1 + role in the status word.
 #include <cstring>
 #include <type_traits>
@@ -961,8 +967,8 @@ Plan plan_fp4(int64_t M, int64_t N, int64_t K) {
         // waves under 95 % busy, for k-loops of 48 blocks or more, with eight or
         // more for every pair: parking and adding the pieces takes about 10 us.
         // Whole / split (us): 1024 x 7168 x 28672 (112 blocks) 106 / 92, 4096 x
-        // 12288 x 12288 (48) 255 / 253, 1024 x 7168 x 7168 (28) 31.6 / 33.8, 2048 x
-        // 4096 x 4096 (16) 21.4 / 31.2.
+        // 12288 x 12288 (48, where the two are even) 255 / 253, 1024 x 7168 x 7168 (28)
+        // 31.6 / 33.8, 2048 x 4096 x 4096 (16) 21.4 / 31.2.
         const int64_t rem = ptiles % pairs, waves = (ptiles + pairs - 1) / pairs;
         if (ptiles > pairs && rem > 0 && 4 * rem <= 3 * pairs && 20 * ptiles < 19 * waves * pairs &&
             kb >= 48 && rem * kb >= 8 * pairs && rem * kb < (1ll << 31) && rem <= kMaxSplitTiles) {

@@ -14,9 +14,10 @@
 // Warps are dealt to spans of `span` flattened tokens and pick the tokens that
 // start a block (or a sequence) there; up to 8 x 512 bytes of the tokens stay in
 // registers between the maximum and the codes.
-// What bounds it: the bytes for prompts (4 of up to 2048 tokens, 8 heads of 128:
-// 10.5 us, 3.3 TB/s), the chain of dependent loads (sequence range, length, block
-// number, scale) for single tokens (64 of them: 3.5 us).
+// What bounds it: the chain of dependent loads (sequence range, length, block
+// number, scale), all of it for single tokens (64 of them: 3.3 us); for prompts a
+// warp's loads of its tokens wait behind it, and the copies run at half the copy
+// rate (4 of up to 2048 tokens, 8 heads of 128: 10.6 us, 3.3 TB/s, 5.4 us of bytes).
 #include "sq_common.cuh"
 #include "sq_kv8.cuh"
 

@@ -33,8 +33,12 @@
 // bytes and by the conversions, so the products are mma.m16n8k16 with the keys
 // (K) and the columns (V) on the 16-wide side and 8 rows on the other: half the
 // instructions and registers of the usual orientation.
-// Measured (32 heads over 8, D 128): 64 sequences of up to 8192 keys 106 us, 5.5 TB/s
-// (0.84 of the copy rate); one of 1000 keys 10.5 us, the chain of loads and the join.
+// Measured (32 heads over 8, D 128): 64 sequences of up to 8192 keys 107 us, 5.4 TB/s
+// (0.83 of the copy rate); one of 1000 keys 11.2 us, the chain of loads and the join.
+// Rows past 16 of a head are further row tiles, which read and convert the keys
+// again: 16 sequences on 4000 keys (20 us of bytes) take 48 us with 4 tokens each,
+// 75 with 8 and 133 with 16. At D = 128 the kernel of two row groups spills (152
+// bytes stored, 248 loaded per thread).
 #include <cstring>
 
 #include "sq_internal.h"
@@ -54,7 +58,10 @@ constexpr int parts_of(int d) { return d == 64 ? 2 : 1; }
 constexpr int kCWarps = 4;    // consumer warps
 constexpr int kThreadsA = 32 * (kCWarps + 1);
 constexpr int kStages = 3;
-// sequences of more rows than this go to the prompt kernel where one is launched
+// Sequences of more rows than this go to the prompt kernel where one is launched.
+// Here / there (us), D = 128, 8 heads: 1 sequence on 8192 keys, 16 rows 23.7 / 48.2, 64
+// rows 32 / 48; 4 on 4000, 64 rows 44 / 45; 16 on 4000, 48 rows 106 / 112, 64 rows
+// 133 / 112. D = 64, 4 heads, 64 rows: 1 on 8192 16 / 36, 16 on 4000 43 / 71.
 constexpr int64_t kRowLimit = 64;
 // blocks per SM by row groups of 8: registers (accumulators) and shared memory
 constexpr int ctas_per_sm(int nr) { return nr == 1 ? 3 : 2; }

@@ -113,7 +113,7 @@ inline bool make_map_kv(CUtensorMap* m, const int8_t* base, int64_t num_blocks, 
               CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Prompts: sequences of more than kv8_row_limit rows (kv8_prefill.cu), and the
+// Prompts: sequences of more rows than row_limit (kv8_prefill.cu), and the
 // bytes of its parts.
 size_t kv8_prefill_part_bytes(int64_t D);
 sq_status_t launch_kv8_prefill(const char* name, sq_dtype_t dt, int64_t D, const int8_t* Kc, const int8_t* Vc,
