@@ -487,3 +487,20 @@ def test_refuses_an_unaligned_workspace(L):
     p, odd = ctypes.c_void_p(1 << 20), ctypes.c_void_p((1 << 20) + 8)
     status = L.sq_gemm_fp4(p, p, p, p, 0, 16, 16, 32, p, 1, p, 1, None, 2, p, 16, odd, 256, None)
     assert status == 3 and "workspace must be 16-byte aligned" in L.sq_last_error_string().decode()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dt", DTYPES)
+@pytest.mark.parametrize("M,N,K,ldy", [(60, 957, 128, 968), (300, 41, 96, 48), (2778, 959, 128, 960), (2500, 2489, 12320, 2496)])
+def test_gemm_rows_that_end_inside_16_bytes(M, N, K, ldy, dt):
+    """Widths that are no multiple of 8 in rows that start on 16-byte boundaries (Y a part of a wider matrix): the
+    columns behind Y, up to the next boundary too, keep what they hold."""
+    (xq, xs, qx), xv, rx = exact_operand(M, K, 0, 1)
+    (wq, wsc, qw), wv, rw = exact_operand(N, K, 0, 2)
+    want = (xv @ wv.T) / torch.from_numpy(rx).cuda()[:, None] / torch.from_numpy(rw).cuda()
+    big = torch.full((M + 1, ldy), 7.0, dtype=dt, device="cuda")
+    ws = sq.workspace(sq.SQ_OP_GEMM_FP4, M, N, K)
+    sq.sq_gemm_fp4(xq, xs, wq, wsc, 0, qx, qw, None, big[:M, :N], ws)
+    sq.sq_workspace_status(ws)
+    assert torch.equal(big[:M, :N], want.float().to(dt))
+    assert bool((big[:, N:] == 7).all() and (big[M:] == 7).all())

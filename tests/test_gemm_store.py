@@ -114,3 +114,33 @@ def test_unaligned_rows_take_plain_stores():
     ref = dequant_ref(acc, qx, qw, torch.bfloat16)
     assert np.array_equal(Y.contiguous().view(torch.int16).cpu().numpy(), ref.view(torch.int16).cpu().numpy())
     assert bool((big[:, N:] == SENTINEL).all())
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("M,N,K,ldy", [(3, 1, 16, 8), (129, 41, 64, 48), (300, 523, 272, 528), (257, 1007, 128, 1024),
+                                       (2048, 6137, 256, 6144)])
+@pytest.mark.parametrize("act", [None, sq.SQ_ACT_RELU])
+def test_rows_that_end_inside_16_bytes(dtype, M, N, K, ldy, act):
+    """Widths that are no multiple of 8 in rows that start on 16-byte boundaries (Y a part of a wider matrix): the
+    columns behind Y, up to the next boundary too, keep what they hold."""
+    g = torch.Generator().manual_seed(M + N + K)
+    Xq, Wq = rand_i8((M, K), M + 1).to(DEV), rand_i8((N, K), N + 2).to(DEV)
+    qx = (torch.rand(M, generator=g) * 30 + 20).to(DEV)
+    qw = (torch.rand(N, generator=g) * 300 + 200).to(DEV)
+    ws = sq.workspace(sq.SQ_OP_GEMM, M, N, K)
+    acc = torch.empty((M, N), dtype=torch.int32, device=DEV)
+    sq.sq_gemm_w8a8(Xq, Wq, None, None, None, acc, ws)
+    big = torch.full((M + 1, ldy), SENTINEL, dtype=torch.int16, device=DEV)
+    Y = big.view(dtype)[:M, :N]
+    if act is None:
+        sq.sq_gemm_w8a8(Xq, Wq, qx, qw, None, Y, ws)
+    else:
+        sq.sq_gemm_w8a8_act(Xq, Wq, qx, qw, None, act, Y, ws)
+    torch.cuda.synchronize()
+    sq.sq_workspace_status(ws)
+    ref = dequant_ref(acc, qx, qw, dtype)
+    if act is not None:
+        ref = torch.where(ref > 0, ref, torch.zeros_like(ref))
+    assert torch.equal(Y.contiguous(), ref)
+    assert bool((big[:, N:] == SENTINEL).all()), "a store landed in the padding columns"
+    assert bool((big[M:] == SENTINEL).all()), "a store landed below the last row"

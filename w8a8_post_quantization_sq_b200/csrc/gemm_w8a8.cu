@@ -1002,7 +1002,7 @@ sq_status_t launch_bn(const int8_t* Xq, const int8_t* Wq, int64_t M, int64_t N, 
     const int eb = ep.act_qs ? 1 : (ep.out_dt == SQ_BF16 || ep.out_dt == SQ_F16) ? 2 : 4;
     p.vec_store = ((reinterpret_cast<uintptr_t>(ep.Y) & 15u) == 0) && ((ep.ldy * eb) % 16 == 0);
     // 16-bit outputs of the plain, ReLU and GELU epilogues go out by TMA
-    // store (row and problem strides multiples of 16 bytes, within the
+    // store (widths, row and problem strides multiples of 16 bytes, within the
     // tensor map's limits); SwiGLU's half-width rows keep the plain stores
     CUtensorMap ty;
     memset(&ty, 0, sizeof(ty));

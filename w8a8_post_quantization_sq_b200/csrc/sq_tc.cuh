@@ -198,10 +198,13 @@ inline PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
 
 // 3-D 16-bit output [batch, M, ldy] (problems y_bstride elements apart), box
 // 32 columns x 32 rows x 1, 64-byte swizzle (the staging layout of a chunk).
+// False where a row's 2 N bytes are no multiple of 16: the copy engine clips a
+// store at the next multiple only, and wrote zeros over up to 14 bytes of what
+// lies behind the row. Those outputs keep the plain stores.
 inline bool make_map_y(CUtensorMap* m, void* Y, int64_t M, int64_t N, int64_t ldy, int64_t batch, int64_t y_bstride,
                 bool bf16) {
     auto fn = encode_fn();
-    if (!fn) return false;
+    if (!fn || N % 8 != 0) return false;
     cuuint64_t dims[3] = {(cuuint64_t)N, (cuuint64_t)M, (cuuint64_t)batch};
     cuuint64_t strides[2] = {(cuuint64_t)(ldy * 2), (cuuint64_t)(y_bstride * 2)};
     cuuint32_t box[3] = {32, 32, 1};
