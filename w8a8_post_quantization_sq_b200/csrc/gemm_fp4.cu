@@ -31,7 +31,7 @@
 //     cluster, which adds them up through its shared memory, in part order.
 //     (Parked in global memory and counted by atomics, the parts cost 2.5 us
 //     more: 16 x 4096 x 4096 9.9 us, so 6.2 us.)
-// What bounds it at 4096 x 12288 x 12288 (NVFP4 253-280 us over boxes and ten calls in
+// What bounds it at 4096 x 12288 x 12288 (NVFP4 253-280 us over devices, ten calls in
 // a row, 4.4-4.9 PFLOP/s): called without end, the power cap (990 W, the SM clock at
 // 1.59 of 1.965 GHz, 311 us). In short runs the tensor cores are active 55 % of the
 // cycles and nothing that was measured is full: L2 delivers 11.4 TB/s, where the
